@@ -19,6 +19,11 @@ MGS_MX_RCEIL = 1
 MGS_MAX_GROUPS = 1024
 MGS_DIM1_MAX_K = 131072
 MGS_NOALLOC_SCRATCH_BYTES = 16 << 20
+MGS_FLAG_ACCUMULATE = 4
+MGS_FLAG_FAST_ACCUM = 8
+MGS_OUT_BF16 = 0
+MGS_OUT_F32 = 1
+MGS_MOE_MAX_TOP_K = 64
 
 EXPORTS = (
     "mgs_quant_groups_dim0", "mgs_dim0_workspace_bytes", "mgs_quant_groups_dim0_ws",
@@ -26,7 +31,9 @@ EXPORTS = (
     "mgs_quant_groups_dim0_t", "mgs_quant_experts_dim1",
     "mgs_quant_groups_dim1", "mgs_mx_quant_dim0",
     "mgs_mx_quant_dim1", "mgs_mx_dequant_dim0", "mgs_cast_e4m3",
-    "mgs_copy", "mgs_test_quant_dim0", "mgs_status_string", "mgs_last_hip_error",
+    "mgs_copy", "mgs_moe_rows", "mgs_moe_workspace_bytes", "mgs_moe_dispatch", "mgs_moe_combine",
+    "mgs_moe_combine_grad", "mgs_quant_rows128", "mgs_quant_blocks128", "mgs_mm_block128", "mgs_mm_wgrad",
+    "mgs_test_quant_dim0", "mgs_status_string", "mgs_last_hip_error",
 )
 
 _lock = threading.Lock()
@@ -82,6 +89,19 @@ def lib():
         L.mgs_cast_e4m3.restype = ctypes.c_int
         L.mgs_copy.argtypes = [vp, vp, i64, vp]
         L.mgs_copy.restype = ctypes.c_int
+        for name, types in (("mgs_moe_rows", [i64, i32, i32, i32, ctypes.POINTER(i64)]),
+                            ("mgs_moe_workspace_bytes", [i64, i32, i32, ctypes.POINTER(i64)]),
+                            ("mgs_moe_dispatch", [vp, i64, i64, vp, i32, i32, i32, u32, i64, vp, vp, vp, vp, vp, vp,
+                                                  vp, i64, vp]),
+                            ("mgs_moe_combine", [vp, i64, i64, vp, i64, i32, vp, vp, vp]),
+                            ("mgs_moe_combine_grad", [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, vp]),
+                            ("mgs_quant_rows128", [vp, i64, i64, u32, vp, vp, vp]),
+                            ("mgs_quant_blocks128", [vp, i64, i64, i64, u32, vp, vp, vp, vp, vp]),
+                            ("mgs_mm_block128", [vp, vp, i64, i64, vp, vp, i32, i64, vp, u32, ctypes.c_int, vp, vp]),
+                            ("mgs_mm_wgrad", [vp, vp, vp, vp, i64, i64, i64, vp, i32, u32, ctypes.c_int, vp, vp])):
+            fn = getattr(L, name)
+            fn.argtypes = types
+            fn.restype = ctypes.c_int
         L.mgs_status_string.argtypes = [ctypes.c_int]
         L.mgs_status_string.restype = ctypes.c_char_p
         L.mgs_last_hip_error.argtypes = []

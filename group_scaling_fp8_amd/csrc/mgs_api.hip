@@ -11,18 +11,14 @@
 
 #include "mgs.h"
 #include "mgs_kernels.hpp"
+#include "mgs_status.hpp"
 
 namespace {
 
 thread_local int g_last_hip_error = 0;
 
-int hip_status(hipError_t e) {
-    if (e == hipSuccess) return MGS_OK;
-    g_last_hip_error = (int)e;
-    return MGS_ERR_HIP;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using mgs::aligned;
+using mgs::hip_status;
 
 // The library's own dim0 workspace, used only by calls that pass none: one
 // per (device, stream), so that calls on different streams never share one.
@@ -114,6 +110,12 @@ int check_grouped(const void* x, int64_t M, int64_t K, const int32_t* offsets, i
 
 namespace mgs {
 
+int hip_status(hipError_t e) {
+    if (e == hipSuccess) return MGS_OK;
+    g_last_hip_error = (int)e;
+    return MGS_ERR_HIP;
+}
+
 struct DeviceInfo {
     long long spin_ticks;   // 20 ms of the device wall clock
     int team_max;           // min(kDim0MaxTeam, CU count)
@@ -141,6 +143,8 @@ DeviceInfo device_info() {
     g_dev_ready[dev].store(1, std::memory_order_release);
     return d;
 }
+
+int device_cus() { return device_info().cus; }
 
 // Overrides of two dim0 launch parameters, for tests only (mgs_test_quant_dim0).
 struct Dim0Knobs {

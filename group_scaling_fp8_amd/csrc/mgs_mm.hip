@@ -1,0 +1,390 @@
+// mgs_mm.hip — products of E4M3 matrices with fp32 scales on the matrix cores
+// (gfx950).
+//
+// Both products contract the contiguous dim of two row-major operands:
+//   block128:  y[m, n] = sum_b 1 / (sa[m, b] sb[e, n / 128, b])
+//                        * sum_{k in block b} a[m, k] b[e, n, k]
+//   wgrad:     dw[g][n, k] = 1 / (sa[n, g] sb[k, g]) * sum_{m in g} a_t[n, m] b_t[k, m]
+// block128 sums every block of 128 from zero and adds the scaled partial sum to
+// its fp32 accumulators; wgrad accumulates in place and scales once at the end.
+//
+// Two forms of the inner sums:
+//   exact  the bytes become bf16 (every E4M3 value is one) and go through the
+//          16 x 16 x 32 bf16 instruction, whose sums are binary32.
+//   fast   one 16 x 16 x 128 instruction on the bytes themselves, at twice the
+//          rate. It aligns the products of each eight consecutive k to the
+//          largest of the eight and drops what lies below 2^-13 of it (measured
+//          bit by bit on the card); the sums of the eights are binary32. The
+//          loss is about 5e-5 of a typical sum, a thirtieth of a bf16 output's
+//          own rounding.
+//
+// An instruction's K order is free as long as both operands use the same one,
+// so a lane holds the 16-byte chunks g and g + 4 (g = lane / 16) of its row's
+// 128 bytes.
+#include "mgs_block128_device.hpp"
+#include "mgs_experts.hpp"
+
+namespace mgs {
+
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+constexpr int kBK = 128;                     // bytes of the contraction a step
+constexpr uint32_t kOutOfRange = 0x80000000u;   // an offset past every tile: the load gives zeros
+
+struct MmArgs {
+    const uint8_t* a;        // block128: (M, K); wgrad: (N, M)
+    const float* a_scales;   // block128: (M, nkb); wgrad: (N, G)
+    const uint8_t* b;        // block128: (E, N, K); wgrad: (K, M)
+    const float* b_scales;   // block128: (E, nnb, nkb); wgrad: (K, G)
+    const int32_t* offsets;  // group ends, or null (block128: one group of M rows)
+    int64_t M, N, K;
+    int G;
+    int accumulate;
+    void* out;
+};
+
+// One output tile: rows of operand A down, rows of operand B across.
+struct Tile {
+    const uint8_t* a;        // first row of the tile, at the contraction's start
+    const uint8_t* b;
+    int64_t stride;          // bytes between rows, both operands
+    int a_rows, b_rows;      // valid rows, at least 1
+    int len;                 // bytes of the contraction
+};
+
+// Bytes that a tile's loads may reach; offsets past them read as zeros.
+struct Span {
+    const uint8_t* p;
+    uint32_t bytes;
+};
+
+// 16 bytes a lane from src.p + off into lds + 16 * lane, without registers
+// between. (The buffer type exists in device code only.)
+__device__ __forceinline__ void load16_lds(Span src, uint32_t off, uint8_t* lds) {
+#ifdef __HIP_DEVICE_COMPILE__
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src.p), 0, (int)src.bytes, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
+#endif
+}
+
+// A tile's rows sit in LDS as 128-byte lines whose 16-byte chunks are permuted
+// by the row, so that the 16 rows that a fragment read touches at one chunk
+// fall on different banks.
+__device__ __forceinline__ int swizzle(int row) { return row & 7; }
+
+// Starts the load of one step's rows of 128 bytes into LDS, 16 bytes a lane
+// straight from memory. Rows past the valid ones repeat the last one (their
+// products are never stored); bytes past the contraction's end are zero.
+template <int WAVES, int LOADS>
+__device__ __forceinline__ void load_tile(Span src, const uint32_t (&voff)[LOADS],
+                                          int chunk, int kk, int len, uint8_t* lds, int wave) {
+    const bool inside = kk + chunk * 16 < len;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+        load16_lds(src, inside ? voff[j] + (uint32_t)kk : kOutOfRange, lds + (j * WAVES + wave) * 1024);
+}
+
+__device__ __forceinline__ v8i fragment(const uint8_t* tile, int row, int g) {
+    const uint8_t* line = tile + row * kBK;
+    const v4i lo = *reinterpret_cast<const v4i*>(line + ((g ^ swizzle(row)) * 16));
+    const v4i hi = *reinterpret_cast<const v4i*>(line + (((g + 4) ^ swizzle(row)) * 16));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Eight E4M3 bytes as bf16.
+__device__ __forceinline__ v8b widen(int lo, int hi) {
+    v8b r;
+#ifdef __HIP_DEVICE_COMPILE__
+    const v2b a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const v2b b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const v2b c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const v2b d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    r = v8b{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+#endif
+    return r;
+}
+
+// A fragment as an instruction of the form takes it.
+template <bool FAST>
+struct Operand;
+
+template <>
+struct Operand<true> {
+    v8i v;
+    __device__ __forceinline__ explicit Operand(v8i x) : v(x) {}
+    __device__ __forceinline__ static v4f mfma(const Operand& a, const Operand& b, v4f c) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, c, 0, 0, 0, 0, 0, 0);
+    }
+};
+
+template <>
+struct Operand<false> {
+    v8b v[4];
+    __device__ __forceinline__ explicit Operand(v8i x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = widen(x[2 * i], x[2 * i + 1]);
+    }
+    __device__ __forceinline__ static v4f mfma(const Operand& a, const Operand& b, v4f c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
+        return c;
+    }
+};
+
+// Group ends as the casts read them: a running maximum, clamped to [0, M].
+// Walks the groups 64 at a time; f(g, begin, end) per lane, for g < G.
+template <typename F>
+__device__ __forceinline__ void for_groups(const int32_t* offsets, int G, int64_t M, int align, F f) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int carry = 0;
+    for (int base = 0; base < G; base += kWave) {
+        const int g = base + lane;
+        int raw = 0;
+        if (g < G) raw = offsets ? min(max(offsets[g], 0), (int)M) / align * align : (int)M;
+        const int end = max(wave_prefix_imax(raw), carry);
+        int begin = __shfl_up(end, 1, kWave);
+        if (lane == 0) begin = carry;
+        carry = __shfl(end, kWave - 1, kWave);
+        if (f(g, begin, end, base, carry)) return;
+    }
+}
+
+template <int BM, int BN, int WM, int WN, bool WGRAD, bool FAST, bool F32>
+__global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void mm_kernel(MmArgs p) {
+    constexpr int WAVES = BM / WM * (BN / WN);
+    constexpr int MT = WM / 16, NT = WN / 16;
+    static_assert(WN <= 128 && 128 % WN == 0, "a wave's columns share one scale block");
+    __shared__ __align__(128) uint8_t s_a[2][BM * kBK];
+    __shared__ __align__(128) uint8_t s_b[2][BN * kBK];
+    __shared__ float s_sa[2][WGRAD ? 1 : BM];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
+
+    // ---- which tile ----
+    Tile t;
+    int64_t m0 = 0, n0;      // block128: first row and column; wgrad: first n and k
+    int g = -1, tile_end = 0;
+    const float* sb = nullptr;
+    const int64_t nkb = (p.K + kBK - 1) / kBK;
+    if constexpr (WGRAD) {
+        const int64_t nt = (p.N + BM - 1) / BM, kt = (p.K + BN - 1) / BN;
+        const int64_t L = blockIdx.x, per = nt * kt;
+        g = (int)(L / per);
+        const int64_t r = L - g * per;
+        m0 = r / kt * BM;
+        n0 = (r - r / kt * kt) * BN;
+        int begin = 0, end = 0;
+        for_groups(p.offsets, p.G, p.M, 16, [&](int gg, int b, int e, int base, int) {
+            if (g >= base + kWave) return false;
+            begin = __shfl(b, g - base, kWave);
+            end = __shfl(e, g - base, kWave);
+            return true;
+        });
+        begin = __builtin_amdgcn_readfirstlane(begin);
+        end = __builtin_amdgcn_readfirstlane(end);
+        t.len = end - begin;
+        t.stride = p.M;
+        t.a = p.a + m0 * p.M + begin;
+        t.b = p.b + n0 * p.M + begin;
+        t.a_rows = (int)min((int64_t)BM, p.N - m0);
+        t.b_rows = (int)min((int64_t)BN, p.K - n0);
+    } else {
+        const int64_t nt = (p.N + BN - 1) / BN;
+        // tiles are numbered by group, then column, then row; the rows past
+        // the last group are one more group whose tiles are zeros
+        int64_t L = blockIdx.x, first = 0;
+        int begin = 0, end = 0, last_end = 0;
+        for_groups(p.offsets, p.G, p.M, 1, [&](int gg, int b, int e, int base, int carry) {
+            const int mine = gg < p.G ? (e - b + BM - 1) / BM : 0;
+            const int upto = wave_prefix_sum(mine);
+            const uint64_t past = __ballot((int64_t)upto * nt > L - first);
+            last_end = carry;
+            if (past) {
+                const int at = __builtin_ctzll(past);
+                g = base + at;
+                begin = __shfl(b, at, kWave);
+                end = __shfl(e, at, kWave);
+                first += (int64_t)(__shfl(upto, at, kWave) - __shfl(mine, at, kWave)) * nt;
+                return true;
+            }
+            first += (int64_t)__shfl(upto, kWave - 1, kWave) * nt;
+            return false;
+        });
+        g = __builtin_amdgcn_readfirstlane(g);
+        begin = __builtin_amdgcn_readfirstlane(begin);
+        end = __builtin_amdgcn_readfirstlane(end);
+        if (g < 0) {
+            begin = __builtin_amdgcn_readfirstlane(last_end);
+            end = (int)p.M;
+        }
+        const int64_t mt = ((int64_t)end - begin + BM - 1) / BM, local = L - first;
+        if (local >= mt * nt) return;
+        m0 = begin + (local % mt) * BM;
+        n0 = local / mt * BN;
+        tile_end = end;
+        t.stride = p.K;
+        t.len = g < 0 ? 0 : (int)p.K;
+        t.a = p.a + m0 * p.K;
+        t.b = p.b + ((int64_t)max(g, 0) * p.N + n0) * p.K;
+        t.a_rows = (int)min((int64_t)BM, end - m0);
+        t.b_rows = (int)min((int64_t)BN, p.N - n0);
+        const int64_t nnb = (p.N + 127) / 128;
+        const int64_t bn = min((n0 + wn) / 128, nnb - 1);
+        sb = p.b_scales + ((int64_t)max(g, 0) * nnb + bn) * nkb;
+    }
+
+    // ---- the contraction ----
+    v4f acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+
+    const int lrow = lane / 8;
+    // lanes of one load instruction write 8 lines of 128 bytes in lane order;
+    // lane l fetches the chunk that belongs at its place
+    const int chunk = (lane & 7) ^ swizzle(lrow);
+    uint32_t va[BM / 8 / WAVES], vb[BN / 8 / WAVES];
+#pragma unroll
+    for (int j = 0; j < BM / 8 / WAVES; ++j) {
+        const int r = min((j * WAVES + wave) * 8 + lrow, t.a_rows - 1);
+        va[j] = (uint32_t)(r * t.stride) + chunk * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < BN / 8 / WAVES; ++j) {
+        const int r = min((j * WAVES + wave) * 8 + lrow, t.b_rows - 1);
+        vb[j] = (uint32_t)(r * t.stride) + chunk * 16;
+    }
+    const Span ra{t.a, (uint32_t)((t.a_rows - 1) * t.stride + t.len)};
+    const Span rb{t.b, (uint32_t)((t.b_rows - 1) * t.stride + t.len)};
+    const int steps = (t.len + kBK - 1) / kBK;
+
+    const int srow = min((int)threadIdx.x, t.a_rows - 1);
+    auto row_scale = [&](int k) { return 1.0f / p.a_scales[(m0 + srow) * nkb + k]; };
+    if (steps > 0) {
+        load_tile<WAVES>(ra, va, chunk, 0, t.len, s_a[0], wave);
+        load_tile<WAVES>(rb, vb, chunk, 0, t.len, s_b[0], wave);
+        if constexpr (!WGRAD) {
+            if (threadIdx.x < BM) s_sa[0][threadIdx.x] = row_scale(0);
+        }
+    }
+    const int fr = lane & 15, fg = lane / 16;
+    for (int k = 0; k < steps; ++k) {
+        const int cur = k & 1;
+        __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt(0): this step's bytes are in LDS
+        __syncthreads();
+        float sb_inv = 0.0f;
+        if constexpr (!WGRAD) sb_inv = 1.0f / sb[k];
+        if (k + 1 < steps) {
+            load_tile<WAVES>(ra, va, chunk, (k + 1) * kBK, t.len, s_a[cur ^ 1], wave);
+            load_tile<WAVES>(rb, vb, chunk, (k + 1) * kBK, t.len, s_b[cur ^ 1], wave);
+            if constexpr (!WGRAD) {
+                if (threadIdx.x < BM) s_sa[cur ^ 1][threadIdx.x] = row_scale(k + 1);
+            }
+        }
+        using Op = Operand<FAST>;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const Op fb(fragment(s_b[cur], wn + j * 16 + fr, fg));
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const Op fa(fragment(s_a[cur], wm + i * 16 + fr, fg));
+                if constexpr (WGRAD) {
+                    acc[i][j] = Op::mfma(fb, fa, acc[i][j]);
+                } else {
+                    const v4f part = Op::mfma(fb, fa, v4f{0, 0, 0, 0});
+                    const float f = s_sa[cur][wm + i * 16 + fr] * sb_inv;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(part[c], f, acc[i][j][c]);
+                }
+            }
+        }
+    }
+
+    // ---- store: a lane holds four consecutive columns of row lane % 16 ----
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t r = m0 + wm + i * 16 + fr;
+        if constexpr (WGRAD) {
+            if (r >= p.N) continue;
+            const float ia = 1.0f / p.a_scales[r * p.G + g];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int64_t c = n0 + wn + j * 16 + fg * 4;
+                if (c >= p.K) continue;
+                const int64_t at = ((int64_t)g * p.N + r) * p.K + c;
+                float v[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] = acc[i][j][x] * ia * (1.0f / p.b_scales[(c + x) * p.G + g]);
+                if constexpr (F32) {
+                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+                    float4 old = make_float4(0, 0, 0, 0);
+                    if (p.accumulate) old = *o;
+                    *o = make_float4(old.x + v[0], old.y + v[1], old.z + v[2], old.w + v[3]);
+                } else {
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                        make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+                }
+            }
+        } else {
+            if (r >= tile_end) continue;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int64_t c = n0 + wn + j * 16 + fg * 4;
+                if (c >= p.N) continue;
+                const int64_t at = r * p.N + c;
+                const v4f v = acc[i][j];
+                if constexpr (F32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                        make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+            }
+        }
+    }
+}
+
+template <int BM, int BN, int WM, int WN, bool WGRAD, bool FAST>
+hipError_t launch(const MmArgs& p, bool f32, int64_t blocks, hipStream_t stream) {
+    constexpr int threads = BM / WM * (BN / WN) * 64;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (f32)
+        hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, WGRAD, FAST, true>), dim3((unsigned)blocks), dim3(threads), 0,
+                           stream, p);
+    else
+        hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, WGRAD, FAST, false>), dim3((unsigned)blocks), dim3(threads), 0,
+                           stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mm_block128(const uint8_t* a, const float* a_scales, int64_t M, int64_t K, const uint8_t* b,
+                              const float* b_scales, int64_t E, int64_t N, const int32_t* offsets, bool fast,
+                              bool f32, void* y, int, hipStream_t stream) {
+    const MmArgs p{a, a_scales, b, b_scales, offsets, M, N, K, (int)E, 0, y};
+    // every group, and the rows past the last one, may end inside a tile
+    const int64_t tiles = M / 128 + (offsets ? E + 1 : 1);
+    const int64_t blocks = tiles * ((N + 127) / 128);
+    return fast ? launch<128, 128, 64, 64, false, true>(p, f32, blocks, stream)
+                : launch<128, 128, 64, 64, false, false>(p, f32, blocks, stream);
+}
+
+hipError_t launch_mm_wgrad(const uint8_t* a_t, const float* a_scales_t, const uint8_t* b_t,
+                           const float* b_scales_t, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
+                           int64_t G, bool fast, bool f32, bool accumulate, void* dw, int, hipStream_t stream) {
+    const MmArgs p{a_t, a_scales_t, b_t, b_scales_t, offsets, M, N, K, (int)G, accumulate ? 1 : 0, dw};
+    const int64_t blocks = G * ((N + 127) / 128) * ((K + 127) / 128);
+    return fast ? launch<128, 128, 64, 64, true, true>(p, f32, blocks, stream)
+                : launch<128, 128, 64, 64, true, false>(p, f32, blocks, stream);
+}
+
+}  // namespace mgs

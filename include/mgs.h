@@ -313,6 +313,142 @@ int mgs_cast_e4m3(const float *in, int64_t n, uint8_t *out, void *stream);
  */
 int mgs_copy(const void *src, void *dst, int64_t bytes, void *stream);
 
+/* ---- mixture of experts: token order, block-128 casts, products ----------
+ *
+ * What stands around the casts in a layer of experts: tokens sorted into the
+ * groups that `offsets` describes (and back), and the products that read the
+ * E4M3 bytes and the scales. Every call is asynchronous, takes all memory
+ * from the caller, and can be captured into a graph.
+ *
+ * A slot i = t * top_k + s is the s-th expert choice of token t. An id outside
+ * [0, n_experts) drops its slot. Row counts are not known on the host, so row
+ * arrays have n_rows rows, at least mgs_moe_rows; the rows that no slot takes
+ * (the ends of the groups and the rows past the last one) are zero.
+ */
+#define MGS_MOE_MAX_TOP_K 64
+#define MGS_FLAG_ACCUMULATE 4u /* mgs_mm_wgrad: add to dw (fp32 only) */
+/* Products: sum in the 8-bit matrix instruction, at twice the rate. It aligns
+ * the products of each eight consecutive terms of a contraction to the largest
+ * of them and drops what lies below 2^-13 of it, so a result may be off by
+ * 2^-10 of the sum of its terms' magnitudes (about 5e-5 of a typical result).
+ * Without it every sum is binary32. Small products may ignore it. */
+#define MGS_FLAG_FAST_ACCUM 8u
+enum { MGS_OUT_BF16 = 0, MGS_OUT_F32 = 1 };
+
+/*
+ * Rows that always hold every group: floor((n + min(n_experts, n) *
+ * (align - 1)) / align) * align with n = T * top_k. Host only.
+ * Requirements: T >= 0, 1 <= top_k <= MGS_MOE_MAX_TOP_K,
+ * 1 <= n_experts <= MGS_MAX_GROUPS, align a multiple of 16 up to 4096,
+ * T * top_k < 2^30. The same hold for every mgs_moe call.
+ */
+int mgs_moe_rows(int64_t T, int32_t top_k, int32_t n_experts, int32_t align, int64_t *n_rows);
+
+/* Bytes of workspace that mgs_moe_dispatch needs: 0 up to 8192 slots, else at
+ * most 256 * n_experts. Its contents need no preparation and do not matter
+ * afterwards. Host only. */
+int mgs_moe_workspace_bytes(int64_t T, int32_t top_k, int32_t n_experts, int64_t *bytes);
+
+/*
+ * Sorts tokens by expert; copies and casts them into that order.
+ *   x           (T, D) bf16 (may be NULL when xp and q are).
+ *   expert_ids  (T, top_k) int32.
+ *   flags       0 or MGS_FLAG_POW2_SCALE.
+ *   offsets     (n_experts) int32 end offsets, written: group e holds expert
+ *               e's slots in slot order, filled up to a multiple of align.
+ *   rows        (T, top_k) int32, written: the row of each slot, -1 if dropped.
+ *   slots       (n_rows) int32, written: the slot of each row, -1 if none.
+ *   xp          (n_rows, D) bf16, written: x in expert order; or NULL.
+ *   q, scales   (n_rows, D) E4M3 bytes and (n_rows, ceil(D / 128)) fp32,
+ *               written: mgs_quant_rows128 of xp, from x in one pass; or both
+ *               NULL.
+ * Requirements: D % 8 == 0; x and xp 16-byte aligned, q 8-byte aligned.
+ */
+int mgs_moe_dispatch(const void *x, int64_t T, int64_t D, const int32_t *expert_ids, int32_t top_k,
+                     int32_t n_experts, int32_t align, uint32_t flags, int64_t n_rows, int32_t *offsets,
+                     int32_t *rows, int32_t *slots, void *xp, void *q, float *scales, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+
+/*
+ * Sums each token's rows: y[t] = sum_s weights[t, s] * yp[rows[t, s]], in fp32
+ * and slot order, rounded once to bf16 (y (T, D)). Slots whose row is outside
+ * [0, n_rows) add nothing; a token without slots gets zeros. weights NULL: all
+ * 1, which is the gradient of mgs_moe_dispatch's xp with respect to x.
+ * Requirements: D % 8 == 0; yp and y 16-byte aligned.
+ */
+int mgs_moe_combine(const void *yp, int64_t n_rows, int64_t D, const int32_t *rows, int64_t T, int32_t top_k,
+                    const float *weights, void *y, void *stream);
+
+/*
+ * The gradient of mgs_moe_combine: dyp[rows[t, s]] = bf16(weights[t, s] *
+ * dy[t]) (n_rows, D) with zeros in the rows no slot takes, and dw[t, s] =
+ * <dy[t], yp[rows[t, s]]> (T, top_k) in fp32, 0 for dropped slots. rows and
+ * slots are mgs_moe_dispatch's. Requirements as for mgs_moe_combine.
+ */
+int mgs_moe_combine_grad(const void *dy, const void *yp, int64_t n_rows, int64_t D, const int32_t *rows,
+                         const int32_t *slots, int64_t T, int32_t top_k, const float *weights, void *dyp, float *dw,
+                         void *stream);
+
+/*
+ * Casts with one scale for each row and block of 128 columns: x (M, K) bf16,
+ * q (M, K) E4M3 bytes, scales (M, ceil(K / 128)) fp32; the last block of a row
+ * may be short. The values are mgs_quant_groups_dim1's with those groups.
+ * flags: 0 or MGS_FLAG_POW2_SCALE. Requirements: K % 8 == 0; x 16-byte
+ * aligned, q 8-byte aligned.
+ */
+int mgs_quant_rows128(const void *x, int64_t M, int64_t K, uint32_t flags, void *q, float *scales, void *stream);
+
+/*
+ * Casts with one scale for each block of 128 x 128 of every matrix: w (E, N, K)
+ * bf16, q (E, N, K) E4M3 bytes, scales (E, ceil(N / 128), ceil(K / 128)) fp32;
+ * and, unless NULL (both), the transposes q_t (E, K, N) and scales_t
+ * (E, ceil(K / 128), ceil(N / 128)), which the input gradient's product reads.
+ * flags: 0 or MGS_FLAG_POW2_SCALE. Requirements: N % 16 == 0, K % 16 == 0; w,
+ * q and q_t 16-byte aligned.
+ */
+int mgs_quant_blocks128(const void *w, int64_t E, int64_t N, int64_t K, uint32_t flags, void *q, float *scales,
+                        void *q_t, float *scales_t, void *stream);
+
+/*
+ * Product of cast rows with each group's cast weight, for m in group e:
+ *   y[m, n] = sum_b 1 / (a_scales[m, b] * b_scales[e, n / 128, b])
+ *             * sum_{k in block b} a[m, k] * b[e, n, k]
+ * with fp32 sums, rounded once to the output type.
+ *   a, a_scales  (M, K) E4M3 bytes, (M, ceil(K / 128)) fp32.
+ *   b, b_scales  (n_groups, N, K) E4M3 bytes, (n_groups, ceil(N / 128),
+ *                ceil(K / 128)) fp32.
+ *   offsets      n_groups int32 end offsets along M, any boundaries. Rows past
+ *                the last end give zeros. NULL with n_groups == 1: all M rows.
+ *   flags        0 or MGS_FLAG_FAST_ACCUM.
+ *   out_type     MGS_OUT_BF16 or MGS_OUT_F32.
+ *   y            (M, N), written.
+ * The scales are finite and positive. A row's result does not depend on other
+ * rows. Requirements: N % 16 == 0, K % 16 == 0, K < 2^23 - 256,
+ * n_groups <= MGS_MAX_GROUPS; a, b and y 16-byte aligned. K == 0 gives zeros.
+ */
+int mgs_mm_block128(const void *a, const float *a_scales, int64_t M, int64_t K, const void *b, const float *b_scales,
+                    int32_t n_groups, int64_t N, const int32_t *offsets, uint32_t flags, int out_type, void *y, void *stream);
+
+/*
+ * Weight gradient of every group from two outputs of mgs_quant_groups_dim0_t:
+ *   dw[g][n, k] = 1 / (a_scales_t[n, g] * b_scales_t[k, g])
+ *                 * sum_{m in group g} a_t[n, m] * b_t[k, m]
+ * with fp32 sums.
+ *   a_t, a_scales_t  (N, M) E4M3 bytes, (N, n_groups) fp32: the output gradient.
+ *   b_t, b_scales_t  (K, M) E4M3 bytes, (K, n_groups) fp32: the input.
+ *   offsets          n_groups int32 end offsets along M, multiples of 16 (they
+ *                    are rounded down to them). Columns past the last end are
+ *                    not read as values.
+ *   flags            MGS_FLAG_ACCUMULATE to add to what dw holds,
+ *                    MGS_FLAG_FAST_ACCUM.
+ *   dw               (n_groups, N, K), written; an empty group gives zeros.
+ * Requirements: M, N and K multiples of 16, M < 2^23 - 256, n_groups <=
+ * MGS_MAX_GROUPS; a_t, b_t and dw 16-byte aligned.
+ */
+int mgs_mm_wgrad(const void *a_t, const float *a_scales_t, const void *b_t, const float *b_scales_t, int64_t M,
+                 int64_t N, int64_t K, const int32_t *offsets, int32_t n_groups, uint32_t flags, int out_type,
+                 void *dw, void *stream);
+
 /*
  * TEST ONLY (not part of the product interface): the dim0-family cast with
  * two launch parameters overridden, so tests can reach paths that the

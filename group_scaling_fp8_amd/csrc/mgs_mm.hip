@@ -64,14 +64,30 @@ struct Span {
     uint32_t bytes;
 };
 
-// 16 bytes a lane from src.p + off into lds + 16 * lane, without registers
-// between. (The buffer type exists in device code only.)
-__device__ __forceinline__ void load16_lds(Span src, uint32_t off, uint8_t* lds) {
+// The buffer descriptor of a span: base, size, raw 32-bit data.
+__device__ __forceinline__ v4i descriptor(Span s) {
+    const uint64_t p = reinterpret_cast<uint64_t>(s.p);
+    return v4i{(int)p, (int)(p >> 32) & 0xFFFF, (int)s.bytes, 0x00020000};
+}
+
+// 16 bytes a lane from the descriptor's base + off into lds + 16 * lane, without
+// registers between. Written out because the compiler, which cannot tell the two
+// buffers of a tile apart, otherwise waits for these loads before every read of
+// the other one; load_wait() stands where the bytes are needed.
+__device__ __forceinline__ void load16_lds(v4i rsrc, uint32_t off, uint32_t lds) {
 #ifdef __HIP_DEVICE_COMPILE__
-    const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src.p), 0, (int)src.bytes, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(off), "s"(rsrc), "s"(lds)
+                 : "memory");
 #endif
+}
+
+// All of this wave's loads are done (vmcnt(0)).
+__device__ __forceinline__ void load_wait() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
 // A tile's rows sit in LDS as 128-byte lines whose 16-byte chunks are permuted
@@ -83,19 +99,18 @@ __device__ __forceinline__ int swizzle(int row) { return row & 7; }
 // straight from memory. Rows past the valid ones repeat the last one (their
 // products are never stored); bytes past the contraction's end are zero.
 template <int WAVES, int LOADS>
-__device__ __forceinline__ void load_tile(Span src, const uint32_t (&voff)[LOADS],
-                                          int chunk, int kk, int len, uint8_t* lds, int wave) {
+__device__ __forceinline__ void load_tile(v4i src, const uint32_t (&voff)[LOADS],
+                                          int chunk, int kk, int len, uint32_t lds, int wave) {
     const bool inside = kk + chunk * 16 < len;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j)
         load16_lds(src, inside ? voff[j] + (uint32_t)kk : kOutOfRange, lds + (j * WAVES + wave) * 1024);
 }
 
-__device__ __forceinline__ v8i fragment(const uint8_t* tile, int row, int g) {
-    const uint8_t* line = tile + row * kBK;
-    const v4i lo = *reinterpret_cast<const v4i*>(line + ((g ^ swizzle(row)) * 16));
-    const v4i hi = *reinterpret_cast<const v4i*>(line + (((g + 4) ^ swizzle(row)) * 16));
-    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+// A lane's two chunks of the line at p.
+__device__ __forceinline__ v8i fragment(const uint8_t* p, int lo, int hi) {
+    return __builtin_shufflevector(*reinterpret_cast<const v4i*>(p + lo), *reinterpret_cast<const v4i*>(p + hi), 0, 1, 2,
+                                   3, 4, 5, 6, 7);
 }
 
 // Eight E4M3 bytes as bf16.
@@ -138,6 +153,13 @@ struct Operand<false> {
     }
 };
 
+// A value that every lane holds, in scalar registers (tile addresses, so that a
+// load's base is one scalar descriptor).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
+}
+
 // Group ends as the casts read them: a running maximum, clamped to [0, M].
 // Walks the groups 64 at a time; f(g, begin, end) per lane, for g < G.
 template <typename F>
@@ -156,16 +178,33 @@ __device__ __forceinline__ void for_groups(const int32_t* offsets, int G, int64_
     }
 }
 
+// Workgroups go to the eight XCDs in turn; each XCD takes a run of consecutive
+// tiles, which share rows and columns in its L2.
+__device__ __forceinline__ int64_t tile_of(int b, int blocks) {
+    const int x = b & 7, i = b >> 3, base = blocks >> 3, more = blocks & 7;
+    return (int64_t)x * base + min(x, more) + i;
+}
+
+// Tile `local` of rows x cols tiles, in bands of eight rows walked column by
+// column: 32 consecutive tiles, the workgroups of one XCD at a time, are a patch
+// of 8 x 4 that reads 12 distinct operand tiles (33 as a single column).
+__device__ __forceinline__ void patch(int64_t local, int rows, int cols, int& row, int& col) {
+    const int band = (int)(local / (8 * (int64_t)cols));
+    const int r = (int)(local - (int64_t)band * 8 * cols), high = min(8, rows - band * 8);
+    col = r / high;
+    row = band * 8 + r - col * high;
+}
+
 template <int BM, int BN, int WM, int WN, bool WGRAD, bool FAST, bool F32>
-__global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void mm_kernel(MmArgs p) {
+__global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs p) {
     constexpr int WAVES = BM / WM * (BN / WN);
     constexpr int MT = WM / 16, NT = WN / 16;
     static_assert(WN <= 128 && 128 % WN == 0, "a wave's columns share one scale block");
     __shared__ __align__(128) uint8_t s_a[2][BM * kBK];
     __shared__ __align__(128) uint8_t s_b[2][BN * kBK];
-    __shared__ float s_sa[2][WGRAD ? 1 : BM];
+    __shared__ float s_sa[4][WGRAD ? 1 : BM];
     const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wave = uniform((int)(threadIdx.x / kWave));
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
 
     // ---- which tile ----
@@ -176,11 +215,12 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void mm_kernel(MmArgs p) 
     const int64_t nkb = (p.K + kBK - 1) / kBK;
     if constexpr (WGRAD) {
         const int64_t nt = (p.N + BM - 1) / BM, kt = (p.K + BN - 1) / BN;
-        const int64_t L = blockIdx.x, per = nt * kt;
+        const int64_t L = tile_of(blockIdx.x, gridDim.x), per = nt * kt;
         g = (int)(L / per);
-        const int64_t r = L - g * per;
-        m0 = r / kt * BM;
-        n0 = (r - r / kt * kt) * BN;
+        int row, col;
+        patch(L - g * per, (int)nt, (int)kt, row, col);
+        m0 = (int64_t)row * BM;
+        n0 = (int64_t)col * BN;
         int begin = 0, end = 0;
         for_groups(p.offsets, p.G, p.M, 16, [&](int gg, int b, int e, int base, int) {
             if (g >= base + kWave) return false;
@@ -188,8 +228,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void mm_kernel(MmArgs p) 
             end = __shfl(e, g - base, kWave);
             return true;
         });
-        begin = __builtin_amdgcn_readfirstlane(begin);
-        end = __builtin_amdgcn_readfirstlane(end);
+        begin = uniform(begin);
+        end = uniform(end);
         t.len = end - begin;
         t.stride = p.M;
         t.a = p.a + m0 * p.M + begin;
@@ -200,13 +240,21 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void mm_kernel(MmArgs p) 
         const int64_t nt = (p.N + BN - 1) / BN;
         // tiles are numbered by group, then column, then row; the rows past
         // the last group are one more group whose tiles are zeros
-        int64_t L = blockIdx.x, first = 0;
-        int begin = 0, end = 0, last_end = 0;
-        for_groups(p.offsets, p.G, p.M, 1, [&](int gg, int b, int e, int base, int carry) {
+        int64_t first = 0;
+        int begin = 0, end = 0, last_end = 0, tiles = 0;
+        for_groups(p.offsets, p.G, p.M, 1, [&](int gg, int b, int e, int, int carry) {
+            tiles += gg < p.G ? (e - b + BM - 1) / BM : 0;
+            last_end = carry;
+            return false;
+        });
+        tiles = __shfl(wave_prefix_sum(tiles), kWave - 1, kWave) + ((int)p.M - last_end + BM - 1) / BM;
+        const int64_t total = uniform(tiles) * nt;
+        if (blockIdx.x >= total) return;
+        const int64_t L = tile_of(blockIdx.x, (int)total);
+        for_groups(p.offsets, p.G, p.M, 1, [&](int gg, int b, int e, int base, int) {
             const int mine = gg < p.G ? (e - b + BM - 1) / BM : 0;
             const int upto = wave_prefix_sum(mine);
             const uint64_t past = __ballot((int64_t)upto * nt > L - first);
-            last_end = carry;
             if (past) {
                 const int at = __builtin_ctzll(past);
                 g = base + at;
@@ -218,17 +266,18 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void mm_kernel(MmArgs p) 
             first += (int64_t)__shfl(upto, kWave - 1, kWave) * nt;
             return false;
         });
-        g = __builtin_amdgcn_readfirstlane(g);
-        begin = __builtin_amdgcn_readfirstlane(begin);
-        end = __builtin_amdgcn_readfirstlane(end);
+        g = uniform(g);
+        begin = uniform(begin);
+        end = uniform(end);
+        first = uniform(first);
         if (g < 0) {
-            begin = __builtin_amdgcn_readfirstlane(last_end);
+            begin = uniform(last_end);
             end = (int)p.M;
         }
-        const int64_t mt = ((int64_t)end - begin + BM - 1) / BM, local = L - first;
-        if (local >= mt * nt) return;
-        m0 = begin + (local % mt) * BM;
-        n0 = local / mt * BN;
+        int row, col;
+        patch(L - first, (end - begin + BM - 1) / BM, (int)nt, row, col);
+        m0 = begin + (int64_t)row * BM;
+        n0 = (int64_t)col * BN;
         tile_end = end;
         t.stride = p.K;
         t.len = g < 0 ? 0 : (int)p.K;
@@ -263,51 +312,121 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void mm_kernel(MmArgs p) 
         const int r = min((j * WAVES + wave) * 8 + lrow, t.b_rows - 1);
         vb[j] = (uint32_t)(r * t.stride) + chunk * 16;
     }
-    const Span ra{t.a, (uint32_t)((t.a_rows - 1) * t.stride + t.len)};
-    const Span rb{t.b, (uint32_t)((t.b_rows - 1) * t.stride + t.len)};
+    const v4i ra = descriptor({t.a, (uint32_t)((t.a_rows - 1) * t.stride + t.len)});
+    const v4i rb = descriptor({t.b, (uint32_t)((t.b_rows - 1) * t.stride + t.len)});
     const int steps = (t.len + kBK - 1) / kBK;
 
-    const int srow = min((int)threadIdx.x, t.a_rows - 1);
-    auto row_scale = [&](int k) { return 1.0f / p.a_scales[(m0 + srow) * nkb + k]; };
-    if (steps > 0) {
-        load_tile<WAVES>(ra, va, chunk, 0, t.len, s_a[0], wave);
-        load_tile<WAVES>(rb, vb, chunk, 0, t.len, s_b[0], wave);
-        if constexpr (!WGRAD) {
-            if (threadIdx.x < BM) s_sa[0][threadIdx.x] = row_scale(0);
-        }
-    }
+    // Scales come two steps ahead, in a ring of four: a step's loads are issued
+    // after the scales of the step behind it, so waiting for a scale never waits
+    // for a tile.
+    const float* sa_row = nullptr;
+    float sa_next = 1.0f, sb_next = 1.0f;
+    const int srow = threadIdx.x % BM;
+    if constexpr (!WGRAD) sa_row = p.a_scales + (m0 + min(srow, t.a_rows - 1)) * nkb;
     const int fr = lane & 15, fg = lane / 16;
+    const int a_at = (wm + fr) * kBK, b_at = (wn + fr) * kBK;
+    const int lo = (fg ^ swizzle(fr)) * 16, hi = ((fg + 4) ^ swizzle(fr)) * 16;
+
+    using Op = Operand<FAST>;
+    v8i fa = {}, fb[NT] = {};
+    const uint32_t lds_a = uniform((int)lds_address(s_a)), lds_b = uniform((int)lds_address(s_b));
+    auto start_loads = [&](int k, int buf) {
+        load_tile<WAVES>(ra, va, chunk, k * kBK, t.len, lds_a + buf * (BM * kBK), wave);
+        load_tile<WAVES>(rb, vb, chunk, k * kBK, t.len, lds_b + buf * (BN * kBK), wave);
+    };
+    if (steps > 0) {
+        start_loads(0, 0);
+        if constexpr (!WGRAD) {
+            s_sa[0][srow] = 1.0f / sa_row[0];
+            s_sa[1][srow] = 1.0f / sa_row[min(1, steps - 1)];
+            sb_next = sb[0];
+            sa_next = sa_row[min(2, steps - 1)];
+        }
+        load_wait();
+        __syncthreads();
+        start_loads(1, 1);
+        fa = fragment(s_a[0] + a_at, lo, hi);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fb[j] = fragment(s_b[0] + b_at + j * 16 * kBK, lo, hi);
+    }
+    // The scaled sums of a row's blocks are added while the next row's
+    // instructions run.
+    v4f part[NT];
+    float part_scale = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[j] = v4f{0, 0, 0, 0};
+    auto promote = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(part[j][c], part_scale, acc[i][j][c]);
+    };
+    // One step: the rows of fragments of A in turn, each read while the one
+    // before it is multiplied. The barrier stands before the last two rows,
+    // whose fragments are already in registers: behind it the other buffer is
+    // complete and this one free, so the loads of the step after next and the
+    // first fragments of the next step are on their way during the rest. Steps
+    // past the last one load zeros and are not computed; the body has no branch,
+    // which keeps each row's sums next to its instructions.
     for (int k = 0; k < steps; ++k) {
         const int cur = k & 1;
-        __builtin_amdgcn_s_waitcnt(0x0f70);      // vmcnt(0): this step's bytes are in LDS
-        __syncthreads();
+        const uint8_t *ta = s_a[cur] + a_at, *na = s_a[cur ^ 1] + a_at, *nb = s_b[cur ^ 1] + b_at;
         float sb_inv = 0.0f;
-        if constexpr (!WGRAD) sb_inv = 1.0f / sb[k];
-        if (k + 1 < steps) {
-            load_tile<WAVES>(ra, va, chunk, (k + 1) * kBK, t.len, s_a[cur ^ 1], wave);
-            load_tile<WAVES>(rb, vb, chunk, (k + 1) * kBK, t.len, s_b[cur ^ 1], wave);
-            if constexpr (!WGRAD) {
-                if (threadIdx.x < BM) s_sa[cur ^ 1][threadIdx.x] = row_scale(k + 1);
-            }
+        if constexpr (!WGRAD) {
+            sb_inv = 1.0f / sb_next;
+            sb_next = sb[min(k + 1, steps - 1)];
         }
-        using Op = Operand<FAST>;
+        auto multiply = [&](int i, const v8i& v) {
+            const Op a(v);
+            if constexpr (WGRAD) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const Op fb(fragment(s_b[cur], wn + j * 16 + fr, fg));
+                for (int j = 0; j < NT; ++j) acc[i][j] = Op::mfma(Op(fb[j]), a, acc[i][j]);
+            } else {
+                const float f = s_sa[k & 3][wm + i * 16 + fr] * sb_inv;
+                v4f now[NT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const Op fa(fragment(s_a[cur], wm + i * 16 + fr, fg));
-                if constexpr (WGRAD) {
-                    acc[i][j] = Op::mfma(fb, fa, acc[i][j]);
-                } else {
-                    const v4f part = Op::mfma(fb, fa, v4f{0, 0, 0, 0});
-                    const float f = s_sa[cur][wm + i * 16 + fr] * sb_inv;
+                for (int j = 0; j < NT; ++j) now[j] = Op::mfma(Op(fb[j]), a, v4f{0, 0, 0, 0});
+                promote((i + MT - 1) % MT);
+                if constexpr (FAST) {
+                    // an instruction, then the additions of a sum that an
+                    // earlier one finished
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(part[c], f, acc[i][j][c]);
+                    for (int j = 0; j < NT; ++j) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+                    }
                 }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) part[j] = now[j];
+                part_scale = f;
             }
+        };
+        v8i ahead = {}, last = {};
+#pragma unroll
+        for (int i = 0; i < MT - 2; ++i) {
+            ahead = fragment(ta + (i + 1) * 16 * kBK, lo, hi);
+            if (i == MT - 3) last = fragment(ta + (MT - 1) * 16 * kBK, lo, hi);
+            multiply(i, fa);
+            fa = ahead;
+            __builtin_amdgcn_sched_barrier(0);
         }
+        load_wait();        // the next step's bytes are in LDS
+        __syncthreads();
+        if constexpr (!WGRAD) {
+            s_sa[(k + 2) & 3][srow] = 1.0f / sa_next;
+            sa_next = sa_row[min(k + 3, steps - 1)];
+        }
+        start_loads(k + 2, cur);
+        multiply(MT - 2, fa);
+        __builtin_amdgcn_sched_barrier(0);
+        fa = fragment(na, lo, hi);
+        multiply(MT - 1, last);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fb[j] = fragment(nb + j * 16 * kBK, lo, hi);
+        __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (!WGRAD) promote(MT - 1);
+    load_wait();            // no load into LDS is left behind
 
     // ---- store: a lane holds four consecutive columns of row lane % 16 ----
 #pragma unroll
@@ -372,19 +491,19 @@ hipError_t launch_mm_block128(const uint8_t* a, const float* a_scales, int64_t M
                               bool f32, void* y, int, hipStream_t stream) {
     const MmArgs p{a, a_scales, b, b_scales, offsets, M, N, K, (int)E, 0, y};
     // every group, and the rows past the last one, may end inside a tile
-    const int64_t tiles = M / 128 + (offsets ? E + 1 : 1);
-    const int64_t blocks = tiles * ((N + 127) / 128);
-    return fast ? launch<128, 128, 64, 64, false, true>(p, f32, blocks, stream)
-                : launch<128, 128, 64, 64, false, false>(p, f32, blocks, stream);
+    const int64_t tiles = M / 256 + (offsets ? E + 1 : 1);
+    const int64_t blocks = tiles * ((N + 255) / 256);
+    return fast ? launch<256, 256, 128, 64, false, true>(p, f32, blocks, stream)
+                : launch<256, 128, 64, 64, false, false>(p, f32, tiles * ((N + 127) / 128), stream);
 }
 
 hipError_t launch_mm_wgrad(const uint8_t* a_t, const float* a_scales_t, const uint8_t* b_t,
                            const float* b_scales_t, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
                            int64_t G, bool fast, bool f32, bool accumulate, void* dw, int, hipStream_t stream) {
     const MmArgs p{a_t, a_scales_t, b_t, b_scales_t, offsets, M, N, K, (int)G, accumulate ? 1 : 0, dw};
-    const int64_t blocks = G * ((N + 127) / 128) * ((K + 127) / 128);
-    return fast ? launch<128, 128, 64, 64, true, true>(p, f32, blocks, stream)
-                : launch<128, 128, 64, 64, true, false>(p, f32, blocks, stream);
+    const int64_t blocks = G * ((N + 255) / 256) * ((K + 255) / 256);
+    return fast ? launch<256, 256, 128, 64, true, true>(p, f32, blocks, stream)
+                : launch<256, 256, 128, 64, true, false>(p, f32, blocks, stream);
 }
 
 }  // namespace mgs

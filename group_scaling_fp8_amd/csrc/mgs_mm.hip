@@ -44,6 +44,7 @@ struct MmArgs {
     const float* b_scales;   // block128: (E, nnb, nkb); wgrad: (K, G)
     const int32_t* offsets;  // group ends, or null (block128: one group of M rows)
     int64_t M, N, K;
+    int64_t cols;            // columns of the output
     int G;
     int accumulate;
     void* out;
@@ -56,6 +57,7 @@ struct Tile {
     int64_t stride;          // bytes between rows, both operands
     int a_rows, b_rows;      // valid rows, at least 1
     int len;                 // bytes of the contraction
+    int skip;                // leading bytes of it that belong to another group
 };
 
 // Bytes that a tile's loads may reach; offsets past them read as zeros.
@@ -91,17 +93,20 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 
 // A tile's rows sit in LDS as 128-byte lines whose 16-byte chunks are permuted
-// by the row, so that the 16 rows that a fragment read touches at one chunk
-// fall on different banks.
-__device__ __forceinline__ int swizzle(int row) { return row & 7; }
+// by the row (chunk c of a line stands at c ^ key), so that the eight rows that
+// eight lanes read at one chunk fall on different banks: the key is the row
+// modulo 8, or for B's rows of a bf16 output, which lanes read in runs of four
+// out of eight, the row's bits 0, 1 and 3.
 
 // Starts the load of one step's rows of 128 bytes into LDS, 16 bytes a lane
 // straight from memory. Rows past the valid ones repeat the last one (their
-// products are never stored); bytes past the contraction's end are zero.
+// products are never stored); bytes outside the contraction are zero.
 template <int WAVES, int LOADS>
 __device__ __forceinline__ void load_tile(v4i src, const uint32_t (&voff)[LOADS],
-                                          int chunk, int kk, int len, uint32_t lds, int wave) {
-    const bool inside = kk + chunk * 16 < len;
+                                          int chunk, int kk, int len, int skip, uint32_t lds,
+                                          int wave) {
+    const int at = kk + chunk * 16;
+    const bool inside = at < len && at >= skip;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j)
         load16_lds(src, inside ? voff[j] + (uint32_t)kk : kOutOfRange, lds + (j * WAVES + wave) * 1024);
@@ -178,11 +183,15 @@ __device__ __forceinline__ void for_groups(const int32_t* offsets, int G, int64_
     }
 }
 
-// Workgroups go to the eight XCDs in turn; each XCD takes a run of consecutive
-// tiles, which share rows and columns in its L2.
-__device__ __forceinline__ int64_t tile_of(int b, int blocks) {
-    const int x = b & 7, i = b >> 3, base = blocks >> 3, more = blocks & 7;
-    return (int64_t)x * base + min(x, more) + i;
+// Workgroups go to the eight XCDs in turn. Each XCD takes 32 consecutive tiles
+// (one a CU), which share rows and columns in its L2, then the 32 that are eight
+// such runs on: groups of unequal length spread over all XCDs. What is left of
+// the last 256 is dealt out in eight equal runs.
+__device__ __forceinline__ int64_t tile_of(int b, int tiles) {
+    const int whole = tiles & ~255, x = b & 7;
+    if (b < whole) return (b & ~255) + x * 32 + ((b & 255) >> 3);
+    const int left = tiles - whole;
+    return whole + x * (left >> 3) + min(x, left & 7) + ((b - whole) >> 3);
 }
 
 // Tile `local` of rows x cols tiles, in bands of eight rows walked column by
@@ -202,7 +211,9 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     static_assert(WN <= 128 && 128 % WN == 0, "a wave's columns share one scale block");
     __shared__ __align__(128) uint8_t s_a[2][BM * kBK];
     __shared__ __align__(128) uint8_t s_b[2][BN * kBK];
-    __shared__ float s_sa[4][WGRAD ? 1 : BM];
+    // block128: a ring of four steps' reciprocal scales of the rows; wgrad: the
+    // reciprocal scales of the tile's rows and columns
+    __shared__ __align__(16) float s_scale[WGRAD ? BM + BN : 4 * BM];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform((int)(threadIdx.x / kWave));
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
@@ -210,7 +221,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     // ---- which tile ----
     Tile t;
     int64_t m0 = 0, n0;      // block128: first row and column; wgrad: first n and k
-    int g = -1, tile_end = 0;
+    int64_t row_end, out_row = 0;     // rows past row_end are not stored; first row of the output's matrix
+    int g = -1;
     const float* sb = nullptr;
     const int64_t nkb = (p.K + kBK - 1) / kBK;
     if constexpr (WGRAD) {
@@ -230,10 +242,16 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         });
         begin = uniform(begin);
         end = uniform(end);
-        t.len = end - begin;
+        row_end = p.N;
+        out_row = (int64_t)g * p.N;
+        // steps start on 128-byte lines: a step across two lines of every row
+        // takes twice as long to fetch
+        const int from = (p.M & 127) == 0 ? begin & ~127 : begin;
+        t.skip = begin - from;
+        t.len = end > begin ? end - from : 0;
         t.stride = p.M;
-        t.a = p.a + m0 * p.M + begin;
-        t.b = p.b + n0 * p.M + begin;
+        t.a = p.a + m0 * p.M + from;
+        t.b = p.b + n0 * p.M + from;
         t.a_rows = (int)min((int64_t)BM, p.N - m0);
         t.b_rows = (int)min((int64_t)BN, p.K - n0);
     } else {
@@ -278,8 +296,9 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         patch(L - first, (end - begin + BM - 1) / BM, (int)nt, row, col);
         m0 = begin + (int64_t)row * BM;
         n0 = (int64_t)col * BN;
-        tile_end = end;
+        row_end = end;
         t.stride = p.K;
+        t.skip = 0;
         t.len = g < 0 ? 0 : (int)p.K;
         t.a = p.a + m0 * p.K;
         t.b = p.b + ((int64_t)max(g, 0) * p.N + n0) * p.K;
@@ -300,17 +319,18 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     const int lrow = lane / 8;
     // lanes of one load instruction write 8 lines of 128 bytes in lane order;
     // lane l fetches the chunk that belongs at its place
-    const int chunk = (lane & 7) ^ swizzle(lrow);
+    const int chunk_a = (lane & 7) ^ lrow;
+    const int chunk_b = (lane & 7) ^ (F32 ? lrow : (lrow & 3) | (wave & 1) << 2);
     uint32_t va[BM / 8 / WAVES], vb[BN / 8 / WAVES];
 #pragma unroll
     for (int j = 0; j < BM / 8 / WAVES; ++j) {
         const int r = min((j * WAVES + wave) * 8 + lrow, t.a_rows - 1);
-        va[j] = (uint32_t)(r * t.stride) + chunk * 16;
+        va[j] = (uint32_t)(r * t.stride) + chunk_a * 16;
     }
 #pragma unroll
     for (int j = 0; j < BN / 8 / WAVES; ++j) {
         const int r = min((j * WAVES + wave) * 8 + lrow, t.b_rows - 1);
-        vb[j] = (uint32_t)(r * t.stride) + chunk * 16;
+        vb[j] = (uint32_t)(r * t.stride) + chunk_b * 16;
     }
     const v4i ra = descriptor({t.a, (uint32_t)((t.a_rows - 1) * t.stride + t.len)});
     const v4i rb = descriptor({t.b, (uint32_t)((t.b_rows - 1) * t.stride + t.len)});
@@ -324,21 +344,35 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     const int srow = threadIdx.x % BM;
     if constexpr (!WGRAD) sa_row = p.a_scales + (m0 + min(srow, t.a_rows - 1)) * nkb;
     const int fr = lane & 15, fg = lane / 16;
-    const int a_at = (wm + fr) * kBK, b_at = (wn + fr) * kBK;
-    const int lo = (fg ^ swizzle(fr)) * 16, hi = ((fg + 4) ^ swizzle(fr)) * 16;
+    // Lane row fr of B's fragment j is column col(j, fr) of the tile. For fp32
+    // that is j * 16 + fr: a lane's four sums are 16 bytes. For bf16 it takes two
+    // fragments to make 16 bytes: fragments 2h and 2h + 1 share out 32 columns,
+    // four each in turn.
+    const int a_at = (wm + fr) * kBK;
+    const int b_at = (wn + (F32 ? fr : (fr >> 2) * 8 + (fr & 3))) * kBK;
+    auto b_row = [](int j) { return F32 ? j * 16 : (j >> 1) * 32 + (j & 1) * 4; };
+    const int lo = (fg ^ (fr & 7)) * 16, hi = ((fg + 4) ^ (fr & 7)) * 16;
 
     using Op = Operand<FAST>;
     v8i fa = {}, fb[NT] = {};
     const uint32_t lds_a = uniform((int)lds_address(s_a)), lds_b = uniform((int)lds_address(s_b));
     auto start_loads = [&](int k, int buf) {
-        load_tile<WAVES>(ra, va, chunk, k * kBK, t.len, lds_a + buf * (BM * kBK), wave);
-        load_tile<WAVES>(rb, vb, chunk, k * kBK, t.len, lds_b + buf * (BN * kBK), wave);
+        load_tile<WAVES>(ra, va, chunk_a, k * kBK, t.len, t.skip, lds_a + buf * (BM * kBK), wave);
+        load_tile<WAVES>(rb, vb, chunk_b, k * kBK, t.len, t.skip, lds_b + buf * (BN * kBK), wave);
     };
+    if constexpr (WGRAD) {
+        for (int x = threadIdx.x; x < BM + BN; x += WAVES * 64) {
+            const bool row = x < BM;
+            const int64_t at = row ? m0 + min(x, t.a_rows - 1) : n0 + min(x - BM, t.b_rows - 1);
+            s_scale[x] = 1.0f / (row ? p.a_scales : p.b_scales)[at * p.G + g];
+        }
+        if (steps == 0) __syncthreads();
+    }
     if (steps > 0) {
         start_loads(0, 0);
         if constexpr (!WGRAD) {
-            s_sa[0][srow] = 1.0f / sa_row[0];
-            s_sa[1][srow] = 1.0f / sa_row[min(1, steps - 1)];
+            s_scale[srow] = 1.0f / sa_row[0];
+            s_scale[BM + srow] = 1.0f / sa_row[min(1, steps - 1)];
             sb_next = sb[0];
             sa_next = sa_row[min(2, steps - 1)];
         }
@@ -347,7 +381,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         start_loads(1, 1);
         fa = fragment(s_a[0] + a_at, lo, hi);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) fb[j] = fragment(s_b[0] + b_at + j * 16 * kBK, lo, hi);
+        for (int j = 0; j < NT; ++j) fb[j] = fragment(s_b[0] + b_at + b_row(j) * kBK, lo, hi);
     }
     // The scaled sums of a row's blocks are added while the next row's
     // instructions run.
@@ -382,7 +416,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
 #pragma unroll
                 for (int j = 0; j < NT; ++j) acc[i][j] = Op::mfma(Op(fb[j]), a, acc[i][j]);
             } else {
-                const float f = s_sa[k & 3][wm + i * 16 + fr] * sb_inv;
+                const float f = s_scale[(k & 3) * BM + wm + i * 16 + fr] * sb_inv;
                 v4f now[NT];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) now[j] = Op::mfma(Op(fb[j]), a, v4f{0, 0, 0, 0});
@@ -413,7 +447,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         load_wait();        // the next step's bytes are in LDS
         __syncthreads();
         if constexpr (!WGRAD) {
-            s_sa[(k + 2) & 3][srow] = 1.0f / sa_next;
+            s_scale[((k + 2) & 3) * BM + srow] = 1.0f / sa_next;
             sa_next = sa_row[min(k + 3, steps - 1)];
         }
         start_loads(k + 2, cur);
@@ -422,50 +456,48 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         fa = fragment(na, lo, hi);
         multiply(MT - 1, last);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) fb[j] = fragment(nb + j * 16 * kBK, lo, hi);
+        for (int j = 0; j < NT; ++j) fb[j] = fragment(nb + b_row(j) * kBK, lo, hi);
         __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!WGRAD) promote(MT - 1);
     load_wait();            // no load into LDS is left behind
 
-    // ---- store: a lane holds four consecutive columns of row lane % 16 ----
+    // ---- store: 16 bytes a lane, 64 contiguous bytes of a row by four lanes ----
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int64_t r = m0 + wm + i * 16 + fr;
-        if constexpr (WGRAD) {
-            if (r >= p.N) continue;
-            const float ia = 1.0f / p.a_scales[r * p.G + g];
+        if (r >= row_end) continue;
+        float ia = 1.0f;
+        if constexpr (WGRAD) ia = s_scale[wm + i * 16 + fr];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int64_t c = n0 + wn + j * 16 + fg * 4;
-                if (c >= p.K) continue;
-                const int64_t at = ((int64_t)g * p.N + r) * p.K + c;
-                float v[4];
+        for (int j = 0; j < NT; j += F32 ? 1 : 2) {
+            const int tc = wn + (F32 ? j * 16 + fg * 4 : j * 16 + fg * 8);
+            const int64_t c = n0 + tc;
+            if (c >= p.cols) continue;
+            const int64_t at = (out_row + r) * p.cols + c;
+            if constexpr (F32) {
+                v4f v = acc[i][j];
+                if constexpr (WGRAD) {
+                    const v4f ib = *reinterpret_cast<const v4f*>(&s_scale[BM + tc]);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[x] = acc[i][j][x] * ia * (1.0f / p.b_scales[(c + x) * p.G + g]);
-                if constexpr (F32) {
-                    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-                    float4 old = make_float4(0, 0, 0, 0);
-                    if (p.accumulate) old = *o;
-                    *o = make_float4(old.x + v[0], old.y + v[1], old.z + v[2], old.w + v[3]);
-                } else {
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-                        make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+                    for (int x = 0; x < 4; ++x) v[x] = v[x] * ia * ib[x];
                 }
-            }
-        } else {
-            if (r >= tile_end) continue;
+                v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(p.out) + at);
+                if (WGRAD && p.accumulate) v += *o;
+                *o = v;
+            } else {
+                v4f u = acc[i][j], v = acc[i][j + 1];
+                if constexpr (WGRAD) {
+                    const v4f iu = *reinterpret_cast<const v4f*>(&s_scale[BM + tc]);
+                    const v4f iv = *reinterpret_cast<const v4f*>(&s_scale[BM + tc + 4]);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int64_t c = n0 + wn + j * 16 + fg * 4;
-                if (c >= p.N) continue;
-                const int64_t at = r * p.N + c;
-                const v4f v = acc[i][j];
-                if constexpr (F32)
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-                else
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-                        make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+                    for (int x = 0; x < 4; ++x) {
+                        u[x] = u[x] * ia * iu[x];
+                        v[x] = v[x] * ia * iv[x];
+                    }
+                }
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) =
+                    make_uint4(bf16x2(u[0], u[1]), bf16x2(u[2], u[3]), bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
             }
         }
     }
@@ -489,7 +521,7 @@ hipError_t launch(const MmArgs& p, bool f32, int64_t blocks, hipStream_t stream)
 hipError_t launch_mm_block128(const uint8_t* a, const float* a_scales, int64_t M, int64_t K, const uint8_t* b,
                               const float* b_scales, int64_t E, int64_t N, const int32_t* offsets, bool fast,
                               bool f32, void* y, int, hipStream_t stream) {
-    const MmArgs p{a, a_scales, b, b_scales, offsets, M, N, K, (int)E, 0, y};
+    const MmArgs p{a, a_scales, b, b_scales, offsets, M, N, K, N, (int)E, 0, y};
     // every group, and the rows past the last one, may end inside a tile
     const int64_t tiles = M / 256 + (offsets ? E + 1 : 1);
     const int64_t blocks = tiles * ((N + 255) / 256);
@@ -500,7 +532,7 @@ hipError_t launch_mm_block128(const uint8_t* a, const float* a_scales, int64_t M
 hipError_t launch_mm_wgrad(const uint8_t* a_t, const float* a_scales_t, const uint8_t* b_t,
                            const float* b_scales_t, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
                            int64_t G, bool fast, bool f32, bool accumulate, void* dw, int, hipStream_t stream) {
-    const MmArgs p{a_t, a_scales_t, b_t, b_scales_t, offsets, M, N, K, (int)G, accumulate ? 1 : 0, dw};
+    const MmArgs p{a_t, a_scales_t, b_t, b_scales_t, offsets, M, N, K, K, (int)G, accumulate ? 1 : 0, dw};
     const int64_t blocks = G * ((N + 255) / 256) * ((K + 255) / 256);
     return fast ? launch<256, 256, 128, 64, true, true>(p, f32, blocks, stream)
                 : launch<256, 256, 128, 64, true, false>(p, f32, blocks, stream);

@@ -15,6 +15,7 @@ using mgs::hip_status;
 // Rows of one operand's tile are addressed with 32-bit offsets: 256 rows of
 // up to this many bytes.
 constexpr int64_t kMaxRowBytes = (int64_t(1) << 31) / 256 - 256;
+constexpr int64_t kMaxCols = kMaxRowBytes / 4;       // of an output
 
 int check_order(int64_t T, int32_t top_k, int32_t n_experts, int32_t align) {
     if (T < 0 || top_k < 1 || n_experts < 1 || align < 16 || align % 16 != 0) return MGS_ERR_INVALID_ARG;
@@ -137,7 +138,7 @@ int mgs_mm_block128(const void* a, const float* a_scales, int64_t M, int64_t K, 
     if (out_type != MGS_OUT_BF16 && out_type != MGS_OUT_F32) return MGS_ERR_INVALID_ARG;
     if (flags & ~MGS_FLAG_FAST_ACCUM) return MGS_ERR_INVALID_ARG;
     if (!offsets && n_groups != 1) return MGS_ERR_INVALID_ARG;
-    if (n_groups > MGS_MAX_GROUPS || M > INT32_MAX || N > INT32_MAX || K > kMaxRowBytes) return MGS_ERR_UNSUPPORTED;
+    if (n_groups > MGS_MAX_GROUPS || M > INT32_MAX || N > kMaxCols || K > kMaxRowBytes) return MGS_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return MGS_OK;
     if (!y || !aligned(y, 16) || !aligned(offsets, 4)) return MGS_ERR_INVALID_ARG;
     if (K > 0 && (!a || !a_scales || !b || !b_scales || !aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) ||
@@ -157,7 +158,7 @@ int mgs_mm_wgrad(const void* a_t, const float* a_scales_t, const void* b_t, cons
     if (flags & ~(MGS_FLAG_ACCUMULATE | MGS_FLAG_FAST_ACCUM)) return MGS_ERR_INVALID_ARG;
     if (out_type != MGS_OUT_BF16 && out_type != MGS_OUT_F32) return MGS_ERR_INVALID_ARG;
     if ((flags & MGS_FLAG_ACCUMULATE) && out_type != MGS_OUT_F32) return MGS_ERR_INVALID_ARG;
-    if (n_groups > MGS_MAX_GROUPS || N > INT32_MAX || K > INT32_MAX || M > kMaxRowBytes) return MGS_ERR_UNSUPPORTED;
+    if (n_groups > MGS_MAX_GROUPS || N > INT32_MAX || K > kMaxCols || M > kMaxRowBytes) return MGS_ERR_UNSUPPORTED;
     if (N == 0 || K == 0) return MGS_OK;
     if (!offsets || !aligned(offsets, 4) || !dw || !aligned(dw, 16)) return MGS_ERR_INVALID_ARG;
     if (!a_scales_t || !b_scales_t || !aligned(a_scales_t, 4) || !aligned(b_scales_t, 4)) return MGS_ERR_INVALID_ARG;

@@ -52,24 +52,21 @@ struct MmArgs {
 
 // One output tile: rows of operand A down, rows of operand B across.
 struct Tile {
-    const uint8_t* a;        // first row of the tile, at the contraction's start
-    const uint8_t* b;
-    int64_t stride;          // bytes between rows, both operands
-    int a_rows, b_rows;      // valid rows, at least 1
+    v4i a, b;                // descriptors that start at the tile's first row
     int len;                 // bytes of the contraction
     int skip;                // leading bytes of it that belong to another group
+    int64_t m0, n0;          // block128: first row and column; wgrad: first n and k
+    int64_t row_end;         // rows past it are not stored
+    int64_t out_row;         // first row of the output's matrix
+    int64_t a_scale, b_scale;   // block128: index of the first row's and of the columns' first scale
+    int g;
 };
 
-// Bytes that a tile's loads may reach; offsets past them read as zeros.
-struct Span {
-    const uint8_t* p;
-    uint32_t bytes;
-};
-
-// The buffer descriptor of a span: base, size, raw 32-bit data.
-__device__ __forceinline__ v4i descriptor(Span s) {
-    const uint64_t p = reinterpret_cast<uint64_t>(s.p);
-    return v4i{(int)p, (int)(p >> 32) & 0xFFFF, (int)s.bytes, 0x00020000};
+// The buffer descriptor of the bytes from p + at to the end of an array of size
+// bytes: base, size, raw 32-bit data. Loads past the end give zeros.
+__device__ __forceinline__ v4i descriptor(const uint8_t* p, int64_t at, int64_t size) {
+    const uint64_t base = reinterpret_cast<uint64_t>(p) + (uint64_t)at;
+    return v4i{(int)base, (int)(base >> 32) & 0xFFFF, (int)min(size - at, (int64_t)0x7FFFFFFF), 0x00020000};
 }
 
 // 16 bytes a lane from the descriptor's base + off into lds + 16 * lane, without
@@ -82,6 +79,19 @@ __device__ __forceinline__ void load16_lds(v4i rsrc, uint32_t off, uint32_t lds)
                  :
                  : "v"(off), "s"(rsrc), "s"(lds)
                  : "memory");
+#endif
+}
+
+// 16 bytes a lane to the descriptor's base + off, as output written once; with
+// `add`, added to the four binary32 values there.
+__device__ __forceinline__ void store16(v4i rsrc, uint32_t off, v4i v, bool add) {
+#ifdef __HIP_DEVICE_COMPILE__
+    typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+    const uint64_t base = (uint32_t)rsrc[0] | (uint64_t)(uint32_t)rsrc[1] << 32;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, rsrc[2], rsrc[3]);
+    if (add) v = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, v) +
+                                             __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0)));
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, off, 0, kLoadNontemporal);
 #endif
 }
 
@@ -101,15 +111,18 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // Starts the load of one step's rows of 128 bytes into LDS, 16 bytes a lane
 // straight from memory. Rows past the valid ones repeat the last one (their
 // products are never stored); bytes outside the contraction are zero.
-template <int WAVES, int LOADS>
-__device__ __forceinline__ void load_tile(v4i src, const uint32_t (&voff)[LOADS],
-                                          int chunk, int kk, int len, int skip, uint32_t lds,
-                                          int wave) {
+template <int WAVES, int ROWS>
+__device__ __forceinline__ void load_tile(v4i src, uint32_t voff, uint32_t stride, int chunk, int kk, int len, int skip,
+                                          uint32_t lds, int wave) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("" : "+s"(kk));        // offsets are made here, not kept in registers for each kk
+#endif
     const int at = kk + chunk * 16;
     const bool inside = at < len && at >= skip;
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j)
-        load16_lds(src, inside ? voff[j] + (uint32_t)kk : kOutOfRange, lds + (j * WAVES + wave) * 1024);
+    for (int j = 0; j < ROWS / 8 / WAVES; ++j)
+        load16_lds(src, inside ? voff + (j * WAVES * 8 * stride + (uint32_t)kk) : kOutOfRange,
+                   lds + (j * WAVES + wave) * 1024);
 }
 
 // A lane's two chunks of the line at p.
@@ -165,29 +178,54 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
 }
 
-// Group ends as the casts read them: a running maximum, clamped to [0, M].
-// Walks the groups 64 at a time; f(g, begin, end) per lane, for g < G.
-template <typename F>
-__device__ __forceinline__ void for_groups(const int32_t* offsets, int G, int64_t M, int align, F f) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int carry = 0;
-    for (int base = 0; base < G; base += kWave) {
-        const int g = base + lane;
-        int raw = 0;
-        if (g < G) raw = offsets ? min(max(offsets[g], 0), (int)M) / align * align : (int)M;
-        const int end = max(wave_prefix_imax(raw), carry);
-        int begin = __shfl_up(end, 1, kWave);
-        if (lane == 0) begin = carry;
-        carry = __shfl(end, kWave - 1, kWave);
-        if (f(g, begin, end, base, carry)) return;
-    }
+// One value for all lanes through the scalar cache, so that waiting for it does
+// not wait for vector loads.
+__device__ __forceinline__ float scalar_load(const float* p) {
+    const uint64_t at = (uint64_t)uniform((int64_t)reinterpret_cast<uint64_t>(p));
+    return *reinterpret_cast<const __attribute__((address_space(4))) float*>(at);
 }
+
+// The groups as the casts read their ends (a running maximum, clamped to [0, M],
+// rounded down to `align`; offsets null: one group of all rows), and the number
+// of tiles of `rows` rows up to each. One wave writes them, 64 groups a turn.
+struct Groups {
+    int end[kMaxGroups];
+    int upto[kMaxGroups];
+
+    __device__ __forceinline__ void fill(const int32_t* offsets, int G, int M, int align, int rows) {
+        const int lane = threadIdx.x & (kWave - 1);
+        int carry = 0, tiles = 0;
+        for (int g = lane; g - lane < G; g += kWave) {
+            int raw = 0;
+            if (g < G) raw = offsets ? min(max(offsets[g], 0), M) / align * align : M;
+            const int e = max(wave_prefix_imax(raw), carry);
+            int b = __shfl_up(e, 1, kWave);
+            if (lane == 0) b = carry;
+            const int u = tiles + wave_prefix_sum((e - b + rows - 1) / rows);
+            if (g < G) {
+                end[g] = e;
+                upto[g] = u;
+            }
+            carry = __shfl(e, kWave - 1, kWave);
+            tiles = __shfl(u, kWave - 1, kWave);
+        }
+    }
+    // The first group with more than `tiles` row tiles up to it, or -1.
+    __device__ __forceinline__ int find(int tiles, int G) const {
+        const int lane = threadIdx.x & (kWave - 1);
+        for (int base = 0; base < G; base += kWave) {
+            const uint64_t past = __ballot(base + lane < G && upto[min(base + lane, G - 1)] > tiles);
+            if (past) return base + __builtin_ctzll(past);
+        }
+        return -1;
+    }
+};
 
 // Workgroups go to the eight XCDs in turn. Each XCD takes 32 consecutive tiles
 // (one a CU), which share rows and columns in its L2, then the 32 that are eight
 // such runs on: groups of unequal length spread over all XCDs. What is left of
 // the last 256 is dealt out in eight equal runs.
-__device__ __forceinline__ int64_t tile_of(int b, int tiles) {
+__device__ __forceinline__ int tile_of(int b, int tiles) {
     const int whole = tiles & ~255, x = b & 7;
     if (b < whole) return (b & ~255) + x * 32 + ((b & 255) >> 3);
     const int left = tiles - whole;
@@ -197,152 +235,149 @@ __device__ __forceinline__ int64_t tile_of(int b, int tiles) {
 // Tile `local` of rows x cols tiles, in bands of eight rows walked column by
 // column: 32 consecutive tiles, the workgroups of one XCD at a time, are a patch
 // of 8 x 4 that reads 12 distinct operand tiles (33 as a single column).
-__device__ __forceinline__ void patch(int64_t local, int rows, int cols, int& row, int& col) {
-    const int band = (int)(local / (8 * (int64_t)cols));
-    const int r = (int)(local - (int64_t)band * 8 * cols), high = min(8, rows - band * 8);
+__device__ __forceinline__ void patch(int local, int rows, int cols, int& row, int& col) {
+    const int band = local / (8 * cols);
+    const int r = local - band * 8 * cols, high = min(8, rows - band * 8);
     col = r / high;
     row = band * 8 + r - col * high;
 }
 
+// Waits until at most `some` (not `none`) or no memory operations of this wave
+// are outstanding. A branch that the compiler does not see keeps a step's body
+// one block.
+template <int SOME>
+__device__ __forceinline__ void wait_some_or_none(int some) {
+    static_assert(SOME < 64, "six bits");
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("v_readfirstlane_b32 vcc_lo, %0\n\ts_cmp_eq_u32 vcc_lo, 0\n\ts_cbranch_scc1 0f\n\t"
+                 "s_waitcnt vmcnt(%1)\n\ts_branch 1f\n0:\n\ts_waitcnt vmcnt(0)\n1:"
+                 :
+                 : "v"(some), "n"(SOME)
+                 : "memory", "scc", "vcc");
+#endif
+}
+
+// One workgroup a CU walks tiles b, b + grid, ...: the first loads of a tile are
+// issued before the stores of the one before it, which then drain under the
+// tile's first steps.
 template <int BM, int BN, int WM, int WN, bool WGRAD, bool FAST, bool F32>
 __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs p) {
     constexpr int WAVES = BM / WM * (BN / WN);
     constexpr int MT = WM / 16, NT = WN / 16;
+    constexpr int LOADS = (BM + BN) / 8 / WAVES;           // a wave's loads a step
+    constexpr int STORES = MT * NT / (F32 ? 1 : 2);        // a wave's stores of a whole tile
     static_assert(WN <= 128 && 128 % WN == 0, "a wave's columns share one scale block");
     __shared__ __align__(128) uint8_t s_a[2][BM * kBK];
     __shared__ __align__(128) uint8_t s_b[2][BN * kBK];
     // block128: a ring of four steps' reciprocal scales of the rows; wgrad: the
-    // reciprocal scales of the tile's rows and columns
-    __shared__ __align__(16) float s_scale[WGRAD ? BM + BN : 4 * BM];
+    // reciprocal scales of this and the next tile's rows and columns
+    __shared__ __align__(16) float s_scale[WGRAD ? 2 * (BM + BN) : 4 * BM];
+    __shared__ Groups s_groups;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform((int)(threadIdx.x / kWave));
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
+    const int64_t nkb = (p.K + kBK - 1) / kBK, nnb = (p.N + 127) / 128;
 
-    // ---- which tile ----
-    Tile t;
-    int64_t m0 = 0, n0;      // block128: first row and column; wgrad: first n and k
-    int64_t row_end, out_row = 0;     // rows past row_end are not stored; first row of the output's matrix
-    int g = -1;
-    const float* sb = nullptr;
-    const int64_t nkb = (p.K + kBK - 1) / kBK;
+    // ---- the tiles ----
+    const int row_tiles = (int)((p.N + BM - 1) / BM);                            // wgrad: down one matrix
+    const int col_tiles = (int)(((WGRAD ? p.K : p.N) + BN - 1) / BN);
+    if (wave == 0) s_groups.fill(p.offsets, p.G, (int)p.M, WGRAD ? 16 : 1, BM);
+    __syncthreads();
+    auto end_of = [&](int g) { return g < 0 ? 0 : uniform(s_groups.end[g]); };
+    int total;       // tiles; the host has checked that 32 bits hold them
     if constexpr (WGRAD) {
-        const int64_t nt = (p.N + BM - 1) / BM, kt = (p.K + BN - 1) / BN;
-        const int64_t L = tile_of(blockIdx.x, gridDim.x), per = nt * kt;
-        g = (int)(L / per);
-        int row, col;
-        patch(L - g * per, (int)nt, (int)kt, row, col);
-        m0 = (int64_t)row * BM;
-        n0 = (int64_t)col * BN;
-        int begin = 0, end = 0;
-        for_groups(p.offsets, p.G, p.M, 16, [&](int gg, int b, int e, int base, int) {
-            if (g >= base + kWave) return false;
-            begin = __shfl(b, g - base, kWave);
-            end = __shfl(e, g - base, kWave);
-            return true;
-        });
-        begin = uniform(begin);
-        end = uniform(end);
-        row_end = p.N;
-        out_row = (int64_t)g * p.N;
-        // steps start on 128-byte lines: a step across two lines of every row
-        // takes twice as long to fetch
-        const int from = (p.M & 127) == 0 ? begin & ~127 : begin;
-        t.skip = begin - from;
-        t.len = end > begin ? end - from : 0;
-        t.stride = p.M;
-        t.a = p.a + m0 * p.M + from;
-        t.b = p.b + n0 * p.M + from;
-        t.a_rows = (int)min((int64_t)BM, p.N - m0);
-        t.b_rows = (int)min((int64_t)BN, p.K - n0);
+        total = p.G * row_tiles * col_tiles;
     } else {
-        const int64_t nt = (p.N + BN - 1) / BN;
-        // tiles are numbered by group, then column, then row; the rows past
-        // the last group are one more group whose tiles are zeros
-        int64_t first = 0;
-        int begin = 0, end = 0, last_end = 0, tiles = 0;
-        for_groups(p.offsets, p.G, p.M, 1, [&](int gg, int b, int e, int, int carry) {
-            tiles += gg < p.G ? (e - b + BM - 1) / BM : 0;
-            last_end = carry;
-            return false;
-        });
-        tiles = __shfl(wave_prefix_sum(tiles), kWave - 1, kWave) + ((int)p.M - last_end + BM - 1) / BM;
-        const int64_t total = uniform(tiles) * nt;
-        if (blockIdx.x >= total) return;
-        const int64_t L = tile_of(blockIdx.x, (int)total);
-        for_groups(p.offsets, p.G, p.M, 1, [&](int gg, int b, int e, int base, int) {
-            const int mine = gg < p.G ? (e - b + BM - 1) / BM : 0;
-            const int upto = wave_prefix_sum(mine);
-            const uint64_t past = __ballot((int64_t)upto * nt > L - first);
-            if (past) {
-                const int at = __builtin_ctzll(past);
-                g = base + at;
-                begin = __shfl(b, at, kWave);
-                end = __shfl(e, at, kWave);
-                first += (int64_t)(__shfl(upto, at, kWave) - __shfl(mine, at, kWave)) * nt;
-                return true;
-            }
-            first += (int64_t)__shfl(upto, kWave - 1, kWave) * nt;
-            return false;
-        });
-        g = uniform(g);
-        begin = uniform(begin);
-        end = uniform(end);
-        first = uniform(first);
-        if (g < 0) {
-            begin = uniform(last_end);
-            end = (int)p.M;
-        }
-        int row, col;
-        patch(L - first, (end - begin + BM - 1) / BM, (int)nt, row, col);
-        m0 = begin + (int64_t)row * BM;
-        n0 = (int64_t)col * BN;
-        row_end = end;
-        t.stride = p.K;
-        t.skip = 0;
-        t.len = g < 0 ? 0 : (int)p.K;
-        t.a = p.a + m0 * p.K;
-        t.b = p.b + ((int64_t)max(g, 0) * p.N + n0) * p.K;
-        t.a_rows = (int)min((int64_t)BM, end - m0);
-        t.b_rows = (int)min((int64_t)BN, p.N - n0);
-        const int64_t nnb = (p.N + 127) / 128;
-        const int64_t bn = min((n0 + wn) / 128, nnb - 1);
-        sb = p.b_scales + ((int64_t)max(g, 0) * nnb + bn) * nkb;
+        // the rows past the last group are one more group whose tiles are zeros
+        total = (uniform(s_groups.upto[p.G - 1]) + ((int)p.M - end_of(p.G - 1) + BM - 1) / BM) * col_tiles;
     }
+    auto tile = [&](int b) {
+        const int L = tile_of(b, total);
+        Tile t;
+        int row, col;
+        if constexpr (WGRAD) {
+            const int per = row_tiles * col_tiles;
+            t.g = uniform(L / per);
+            patch(L - t.g * per, row_tiles, col_tiles, row, col);
+            const int begin = end_of(t.g - 1), end = end_of(t.g);
+            // steps start on 128-byte lines: a step across two lines of every
+            // row takes twice as long to fetch
+            const int from = (p.M & 127) == 0 ? begin & ~127 : begin;
+            t.skip = begin - from;
+            t.len = end > begin ? end - from : 0;
+            t.m0 = (int64_t)uniform(row) * BM;
+            t.n0 = (int64_t)uniform(col) * BN;
+            t.row_end = p.N;
+            t.out_row = (int64_t)t.g * p.N;
+            t.a = descriptor(p.a, t.m0 * p.M + from, p.N * p.M);
+            t.b = descriptor(p.b, t.n0 * p.M + from, p.K * p.M);
+            t.a_scale = t.b_scale = 0;
+        } else {
+            // tiles are numbered by group, then in patches
+            t.g = uniform(s_groups.find(uniform(L / col_tiles), p.G));
+            const int last = t.g < 0 ? p.G - 1 : t.g - 1;      // the group before
+            const int begin = end_of(last), end = t.g < 0 ? (int)p.M : end_of(t.g);
+            const int first = last < 0 ? 0 : uniform(s_groups.upto[last]);
+            patch(L - first * col_tiles, (end - begin + BM - 1) / BM, col_tiles, row, col);
+            t.m0 = begin + (int64_t)uniform(row) * BM;
+            t.n0 = (int64_t)uniform(col) * BN;
+            t.row_end = end;
+            t.out_row = 0;
+            t.skip = 0;
+            t.len = t.g < 0 ? 0 : (int)p.K;
+            const int64_t e = max(t.g, 0);
+            t.a = descriptor(p.a, t.m0 * p.K, p.M * p.K);
+            t.b = descriptor(p.b, (e * p.N + t.n0) * p.K, p.G * p.N * p.K);
+            t.a_scale = t.m0 * nkb;
+            t.b_scale = (e * nnb + min((t.n0 + wn) / 128, nnb - 1)) * nkb;
+        }
+        return t;
+    };
+    int b = blockIdx.x;
+    if (b >= total) return;
 
-    // ---- the contraction ----
-    v4f acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-
+    // ---- loads ----
     const int lrow = lane / 8;
     // lanes of one load instruction write 8 lines of 128 bytes in lane order;
     // lane l fetches the chunk that belongs at its place
     const int chunk_a = (lane & 7) ^ lrow;
     const int chunk_b = (lane & 7) ^ (F32 ? lrow : (lrow & 3) | (wave & 1) << 2);
-    uint32_t va[BM / 8 / WAVES], vb[BN / 8 / WAVES];
-#pragma unroll
-    for (int j = 0; j < BM / 8 / WAVES; ++j) {
-        const int r = min((j * WAVES + wave) * 8 + lrow, t.a_rows - 1);
-        va[j] = (uint32_t)(r * t.stride) + chunk_a * 16;
-    }
-#pragma unroll
-    for (int j = 0; j < BN / 8 / WAVES; ++j) {
-        const int r = min((j * WAVES + wave) * 8 + lrow, t.b_rows - 1);
-        vb[j] = (uint32_t)(r * t.stride) + chunk_b * 16;
-    }
-    const v4i ra = descriptor({t.a, (uint32_t)((t.a_rows - 1) * t.stride + t.len)});
-    const v4i rb = descriptor({t.b, (uint32_t)((t.b_rows - 1) * t.stride + t.len)});
-    const int steps = (t.len + kBK - 1) / kBK;
-
+    const uint32_t stride = (uint32_t)(WGRAD ? p.M : p.K);
+    const uint32_t va = (wave * 8 + lrow) * stride + chunk_a * 16, vb = (wave * 8 + lrow) * stride + chunk_b * 16;
+    const uint32_t lds_a = uniform((int)lds_address(s_a)), lds_b = uniform((int)lds_address(s_b));
+    auto start_loads = [&](const Tile& t, int k, int buf) {
+        load_tile<WAVES, BM>(t.a, va, stride, chunk_a, k * kBK, t.len, t.skip, lds_a + buf * (BM * kBK), wave);
+        load_tile<WAVES, BN>(t.b, vb, stride, chunk_b, k * kBK, t.len, t.skip, lds_b + buf * (BN * kBK), wave);
+    };
     // Scales come two steps ahead, in a ring of four: a step's loads are issued
     // after the scales of the step behind it, so waiting for a scale never waits
     // for a tile.
-    const float* sa_row = nullptr;
-    float sa_next = 1.0f, sb_next = 1.0f;
     const int srow = threadIdx.x % BM;
-    if constexpr (!WGRAD) sa_row = p.a_scales + (m0 + min(srow, t.a_rows - 1)) * nkb;
+    uint32_t srow_at = 0;
+    float sa_0 = 1.0f, sa_1 = 1.0f, sa_next = 1.0f, sb_next = 1.0f;
+    auto row_scale = [&](const Tile& t, int k) {
+        return (p.a_scales + t.a_scale + k)[srow_at];
+    };
+    auto start_tile = [&](const Tile& t, int buf) {
+        if constexpr (WGRAD) {
+            const int x = threadIdx.x;          // one scale a thread
+            static_assert(!WGRAD || BM + BN <= WAVES * 64, "rows and columns");
+            const bool down = x < BM;
+            const int64_t at = down ? min(t.m0 + x, p.N - 1) : min(t.n0 + x - BM, p.K - 1);
+            sa_0 = (down ? p.a_scales : p.b_scales)[at * p.G + t.g];
+        } else if (t.len > 0) {
+            const int end = (t.len + kBK - 1) / kBK - 1;
+            srow_at = (uint32_t)min(srow, (int)(p.M - 1 - t.m0)) * (uint32_t)nkb;
+            sa_0 = row_scale(t, 0);
+            sa_1 = row_scale(t, min(1, end));
+            sa_next = row_scale(t, min(2, end));
+            sb_next = scalar_load(p.b_scales + t.b_scale);
+        }
+        start_loads(t, 0, buf);
+        start_loads(t, 1, buf ^ 1);
+    };
+
+    // ---- fragments ----
     const int fr = lane & 15, fg = lane / 16;
     // Lane row fr of B's fragment j is column col(j, fr) of the tile. For fp32
     // that is j * 16 + fr: a lane's four sums are 16 bytes. For bf16 it takes two
@@ -352,36 +387,34 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     const int b_at = (wn + (F32 ? fr : (fr >> 2) * 8 + (fr & 3))) * kBK;
     auto b_row = [](int j) { return F32 ? j * 16 : (j >> 1) * 32 + (j & 1) * 4; };
     const int lo = (fg ^ (fr & 7)) * 16, hi = ((fg + 4) ^ (fr & 7)) * 16;
-
     using Op = Operand<FAST>;
-    v8i fa = {}, fb[NT] = {};
-    const uint32_t lds_a = uniform((int)lds_address(s_a)), lds_b = uniform((int)lds_address(s_b));
-    auto start_loads = [&](int k, int buf) {
-        load_tile<WAVES>(ra, va, chunk_a, k * kBK, t.len, t.skip, lds_a + buf * (BM * kBK), wave);
-        load_tile<WAVES>(rb, vb, chunk_b, k * kBK, t.len, t.skip, lds_b + buf * (BN * kBK), wave);
-    };
-    if constexpr (WGRAD) {
-        for (int x = threadIdx.x; x < BM + BN; x += WAVES * 64) {
-            const bool row = x < BM;
-            const int64_t at = row ? m0 + min(x, t.a_rows - 1) : n0 + min(x - BM, t.b_rows - 1);
-            s_scale[x] = 1.0f / (row ? p.a_scales : p.b_scales)[at * p.G + g];
-        }
-        if (steps == 0) __syncthreads();
-    }
-    if (steps > 0) {
-        start_loads(0, 0);
-        if constexpr (!WGRAD) {
-            s_scale[srow] = 1.0f / sa_row[0];
-            s_scale[BM + srow] = 1.0f / sa_row[min(1, steps - 1)];
-            sb_next = sb[0];
-            sa_next = sa_row[min(2, steps - 1)];
-        }
-        load_wait();
-        __syncthreads();
-        start_loads(1, 1);
-        fa = fragment(s_a[0] + a_at, lo, hi);
+
+    Tile t = tile(b);
+    start_tile(t, 0);
+    int ring = 0;            // steps of the tiles before this one
+    int parity = 0;          // of the tiles walked
+    int drain = 0;           // whether a tile's stores (and nothing else) follow this tile's first loads
+    for (;;) {
+    const int steps = (t.len + kBK - 1) / kBK;
+    v4f acc[MT][NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) fb[j] = fragment(s_b[0] + b_at + b_row(j) * kBK, lo, hi);
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+    float* const scale = s_scale + (WGRAD ? parity * (BM + BN) : 0);
+    if constexpr (WGRAD) {
+        scale[threadIdx.x] = 1.0f / sa_0;
+    } else {
+        scale[(ring & 3) * BM + srow] = 1.0f / sa_0;
+        scale[((ring + 1) & 3) * BM + srow] = 1.0f / sa_1;
+    }
+    wait_some_or_none<STORES + LOADS>(drain);
+    __syncthreads();
+    v8i fa = {}, fb[NT] = {};
+    if (steps > 0) {
+        fa = fragment(s_a[ring & 1] + a_at, lo, hi);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fb[j] = fragment(s_b[ring & 1] + b_at + b_row(j) * kBK, lo, hi);
     }
     // The scaled sums of a row's blocks are added while the next row's
     // instructions run.
@@ -402,13 +435,14 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     // first fragments of the next step are on their way during the rest. Steps
     // past the last one load zeros and are not computed; the body has no branch,
     // which keeps each row's sums next to its instructions.
+#pragma clang loop unroll(disable)
     for (int k = 0; k < steps; ++k) {
-        const int cur = k & 1;
+        const int cur = (ring + k) & 1;
         const uint8_t *ta = s_a[cur] + a_at, *na = s_a[cur ^ 1] + a_at, *nb = s_b[cur ^ 1] + b_at;
         float sb_inv = 0.0f;
         if constexpr (!WGRAD) {
             sb_inv = 1.0f / sb_next;
-            sb_next = sb[min(k + 1, steps - 1)];
+            sb_next = scalar_load(p.b_scales + t.b_scale + min(k + 1, steps - 1));
         }
         auto multiply = [&](int i, const v8i& v) {
             const Op a(v);
@@ -416,7 +450,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
 #pragma unroll
                 for (int j = 0; j < NT; ++j) acc[i][j] = Op::mfma(Op(fb[j]), a, acc[i][j]);
             } else {
-                const float f = s_scale[(k & 3) * BM + wm + i * 16 + fr] * sb_inv;
+                const float f = scale[((ring + k) & 3) * BM + wm + i * 16 + fr] * sb_inv;
                 v4f now[NT];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) now[j] = Op::mfma(Op(fb[j]), a, v4f{0, 0, 0, 0});
@@ -444,13 +478,14 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             fa = ahead;
             __builtin_amdgcn_sched_barrier(0);
         }
-        load_wait();        // the next step's bytes are in LDS
+        // the next step's bytes are in LDS
+        wait_some_or_none<STORES>(k == 0 ? drain : 0);
         __syncthreads();
         if constexpr (!WGRAD) {
-            s_scale[((k + 2) & 3) * BM + srow] = 1.0f / sa_next;
-            sa_next = sa_row[min(k + 3, steps - 1)];
+            scale[((ring + k + 2) & 3) * BM + srow] = 1.0f / sa_next;
+            sa_next = row_scale(t, min(k + 3, steps - 1));
         }
-        start_loads(k + 2, cur);
+        start_loads(t, k + 2, cur);
         multiply(MT - 2, fa);
         __builtin_amdgcn_sched_barrier(0);
         fa = fragment(na, lo, hi);
@@ -460,53 +495,81 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!WGRAD) promote(MT - 1);
-    load_wait();            // no load into LDS is left behind
+    ring += steps;
 
-    // ---- store: 16 bytes a lane, 64 contiguous bytes of a row by four lanes ----
+    // Both buffers are free (every wave has read its last fragments before the
+    // last barrier): the next tile's first loads go out before the stores.
+    const Tile done = t;
+    b += gridDim.x;
+    const bool more = b < total;
+    if (more) {
+        t = tile(b);
+        start_tile(t, ring & 1);
+    }
+    drain = p.accumulate ? 0 : 1;
+    parity ^= 1;
+
+    // ---- store: 16 bytes a lane, whole 128-byte lines by eight lanes ----
+    // A lane has two pieces of 16 bytes of a line: the first of lanes fr + 8 and
+    // the second of lanes fr change places, so that one store holds rows 0-7 of
+    // sixteen and the other rows 8-15. Stores outside the output are dropped by
+    // the descriptor's bounds, so every tile issues the same number of them.
+    const uint32_t pitch = (uint32_t)p.cols * (F32 ? 4 : 2);
+    const int64_t first = (done.out_row + done.m0) * pitch + done.n0 * (F32 ? 4 : 2);
+    const v4i out = descriptor(static_cast<uint8_t*>(p.out), first, (done.out_row + done.row_end) * pitch);
+    uint32_t at[NT / (F32 ? 2 : 4)];
+#pragma unroll
+    for (int j = 0; j < NT / (F32 ? 2 : 4); ++j) {
+        const int c = wn + (fg + (fr >> 3) * 4) * (F32 ? 4 : 8) + j * (F32 ? 32 : 64);
+        at[j] = done.n0 + c < p.cols ? (wm + (fr & 7)) * pitch + c * (F32 ? 4 : 2) : kOutOfRange;
+    }
+    v4f ib[NT];
+    if constexpr (WGRAD) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            ib[j] = *reinterpret_cast<const v4f*>(scale + BM + wn + (F32 ? j * 16 + fg * 4 : (j >> 1) * 32 + fg * 8 + (j & 1) * 4));
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int64_t r = m0 + wm + i * 16 + fr;
-        if (r >= row_end) continue;
-        float ia = 1.0f;
-        if constexpr (WGRAD) ia = s_scale[wm + i * 16 + fr];
+        if constexpr (WGRAD) {
+            const float ia = scale[wm + fr + i * 16];
 #pragma unroll
-        for (int j = 0; j < NT; j += F32 ? 1 : 2) {
-            const int tc = wn + (F32 ? j * 16 + fg * 4 : j * 16 + fg * 8);
-            const int64_t c = n0 + tc;
-            if (c >= p.cols) continue;
-            const int64_t at = (out_row + r) * p.cols + c;
-            if constexpr (F32) {
-                v4f v = acc[i][j];
-                if constexpr (WGRAD) {
-                    const v4f ib = *reinterpret_cast<const v4f*>(&s_scale[BM + tc]);
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) v[x] = v[x] * ia * ib[x];
-                }
-                v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(p.out) + at);
-                if (WGRAD && p.accumulate) v += *o;
-                *o = v;
-            } else {
-                v4f u = acc[i][j], v = acc[i][j + 1];
-                if constexpr (WGRAD) {
-                    const v4f iu = *reinterpret_cast<const v4f*>(&s_scale[BM + tc]);
-                    const v4f iv = *reinterpret_cast<const v4f*>(&s_scale[BM + tc + 4]);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        u[x] = u[x] * ia * iu[x];
-                        v[x] = v[x] * ia * iv[x];
-                    }
-                }
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) =
-                    make_uint4(bf16x2(u[0], u[1]), bf16x2(u[2], u[3]), bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
-            }
+                for (int c = 0; c < 4; ++c) acc[i][j][c] = acc[i][j][c] * ia * ib[j][c];
         }
+#pragma unroll
+        for (int j = 0; j < NT / (F32 ? 2 : 4); ++j) {
+            v4i v[2], w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (F32) {
+                    v[h] = __builtin_bit_cast(v4i, acc[i][2 * j + h]);
+                } else {
+                    const v4f x = acc[i][4 * j + 2 * h], y = acc[i][4 * j + 2 * h + 1];
+                    v[h] = v4i{(int)bf16x2(x[0], x[1]), (int)bf16x2(x[2], x[3]), (int)bf16x2(y[0], y[1]),
+                               (int)bf16x2(y[2], y[3])};
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                // row_ror:8 into the upper, then the lower half of 16 lanes
+                w[0][c] = __builtin_amdgcn_update_dpp(v[0][c], v[1][c], 0x128, 0xF, 0xC, false);
+                w[1][c] = __builtin_amdgcn_update_dpp(v[1][c], v[0][c], 0x128, 0xF, 0x3, false);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) store16(out, at[j] + (i * 16 + h * 8) * pitch, w[h], WGRAD && p.accumulate);
+        }
+    }
+    if (!more) return;
     }
 }
 
 template <int BM, int BN, int WM, int WN, bool WGRAD, bool FAST>
-hipError_t launch(const MmArgs& p, bool f32, int64_t blocks, hipStream_t stream) {
+hipError_t launch(const MmArgs& p, bool f32, int64_t tiles, int cus, hipStream_t stream) {
     constexpr int threads = BM / WM * (BN / WN) * 64;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t blocks = tiles < cus ? tiles : cus;
     if (f32)
         hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, WGRAD, FAST, true>), dim3((unsigned)blocks), dim3(threads), 0,
                            stream, p);
@@ -520,22 +583,22 @@ hipError_t launch(const MmArgs& p, bool f32, int64_t blocks, hipStream_t stream)
 
 hipError_t launch_mm_block128(const uint8_t* a, const float* a_scales, int64_t M, int64_t K, const uint8_t* b,
                               const float* b_scales, int64_t E, int64_t N, const int32_t* offsets, bool fast,
-                              bool f32, void* y, int, hipStream_t stream) {
+                              bool f32, void* y, int cus, hipStream_t stream) {
     const MmArgs p{a, a_scales, b, b_scales, offsets, M, N, K, N, (int)E, 0, y};
     // every group, and the rows past the last one, may end inside a tile
     const int64_t tiles = M / 256 + (offsets ? E + 1 : 1);
     const int64_t blocks = tiles * ((N + 255) / 256);
-    return fast ? launch<256, 256, 128, 64, false, true>(p, f32, blocks, stream)
-                : launch<256, 128, 64, 64, false, false>(p, f32, tiles * ((N + 127) / 128), stream);
+    return fast ? launch<256, 256, 128, 64, false, true>(p, f32, blocks, cus, stream)
+                : launch<256, 128, 64, 64, false, false>(p, f32, tiles * ((N + 127) / 128), cus, stream);
 }
 
 hipError_t launch_mm_wgrad(const uint8_t* a_t, const float* a_scales_t, const uint8_t* b_t,
                            const float* b_scales_t, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
-                           int64_t G, bool fast, bool f32, bool accumulate, void* dw, int, hipStream_t stream) {
+                           int64_t G, bool fast, bool f32, bool accumulate, void* dw, int cus, hipStream_t stream) {
     const MmArgs p{a_t, a_scales_t, b_t, b_scales_t, offsets, M, N, K, K, (int)G, accumulate ? 1 : 0, dw};
     const int64_t blocks = G * ((N + 255) / 256) * ((K + 255) / 256);
-    return fast ? launch<256, 256, 128, 64, true, true>(p, f32, blocks, stream)
-                : launch<256, 256, 128, 64, true, false>(p, f32, blocks, stream);
+    return fast ? launch<256, 256, 128, 64, true, true>(p, f32, blocks, cus, stream)
+                : launch<256, 256, 128, 64, true, false>(p, f32, blocks, cus, stream);
 }
 
 }  // namespace mgs

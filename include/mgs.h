@@ -424,7 +424,7 @@ int mgs_quant_blocks128(const void *w, int64_t E, int64_t N, int64_t K, uint32_t
  *   y            (M, N), written.
  * The scales are finite and positive. A row's result does not depend on other
  * rows. Requirements: N % 16 == 0, K % 16 == 0, K < 2^23 - 256,
- * n_groups <= MGS_MAX_GROUPS; a, b and y 16-byte aligned. K == 0 gives zeros.
+ * N < 2^21 - 64, n_groups <= MGS_MAX_GROUPS; a, b and y 16-byte aligned. K == 0 gives zeros.
  */
 int mgs_mm_block128(const void *a, const float *a_scales, int64_t M, int64_t K, const void *b, const float *b_scales,
                     int32_t n_groups, int64_t N, const int32_t *offsets, uint32_t flags, int out_type, void *y, void *stream);
@@ -442,8 +442,8 @@ int mgs_mm_block128(const void *a, const float *a_scales, int64_t M, int64_t K, 
  *   flags            MGS_FLAG_ACCUMULATE to add to what dw holds,
  *                    MGS_FLAG_FAST_ACCUM.
  *   dw               (n_groups, N, K), written; an empty group gives zeros.
- * Requirements: M, N and K multiples of 16, M < 2^23 - 256, n_groups <=
- * MGS_MAX_GROUPS; a_t, b_t and dw 16-byte aligned.
+ * Requirements: M, N and K multiples of 16, M < 2^23 - 256, K < 2^21 - 64,
+ * n_groups <= MGS_MAX_GROUPS; a_t, b_t and dw 16-byte aligned.
  */
 int mgs_mm_wgrad(const void *a_t, const float *a_scales_t, const void *b_t, const float *b_scales_t, int64_t M,
                  int64_t N, int64_t K, const int32_t *offsets, int32_t n_groups, uint32_t flags, int out_type,

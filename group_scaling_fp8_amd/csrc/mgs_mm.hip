@@ -23,6 +23,7 @@
 // 128 bytes.
 #include "mgs_block128_device.hpp"
 #include "mgs_experts.hpp"
+#include "mgs_kernels.hpp"
 
 namespace mgs {
 
@@ -55,12 +56,15 @@ struct Tile {
     v4i a, b;                // descriptors that start at the tile's first row
     int len;                 // bytes of the contraction
     int skip;                // leading bytes of it that belong to another group
-    int64_t m0, n0;          // block128: first row and column; wgrad: first n and k
-    int64_t row_end;         // rows past it are not stored
-    int64_t out_row;         // first row of the output's matrix
-    int64_t a_scale, b_scale;   // block128: index of the first row's and of the columns' first scale
+    int steps;               // at least kMinSteps: the ones past len multiply zeros
+    int m0, n0;              // block128: first row and column; wgrad: first n and k
+    int row_end;             // rows past it are not stored
     int g;
+    const float *sa, *sb;    // block128: scales of the first row and of the wave's columns
 };
+
+// Loads run two steps ahead of the sums and scales three, at most one tile on.
+constexpr int kMinSteps = 3;
 
 // The buffer descriptor of the bytes from p + at to the end of an array of size
 // bytes: base, size, raw 32-bit data. Loads past the end give zeros.
@@ -75,7 +79,9 @@ __device__ __forceinline__ v4i descriptor(const uint8_t* p, int64_t at, int64_t 
 // the other one; load_wait() stands where the bytes are needed.
 __device__ __forceinline__ void load16_lds(v4i rsrc, uint32_t off, uint32_t lds) {
 #ifdef __HIP_DEVICE_COMPILE__
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+    // (the compiler does not see what the instruction reads: five wait states
+    // stand for a descriptor that a vector instruction has just written)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
                  : "v"(off), "s"(rsrc), "s"(lds)
                  : "memory");
@@ -249,7 +255,8 @@ template <int SOME>
 __device__ __forceinline__ void wait_some_or_none(int some) {
     static_assert(SOME < 64, "six bits");
 #ifdef __HIP_DEVICE_COMPILE__
-    asm volatile("v_readfirstlane_b32 vcc_lo, %0\n\ts_cmp_eq_u32 vcc_lo, 0\n\ts_cbranch_scc1 0f\n\t"
+    // (a lane read needs a wait state after the instruction that wrote the lane)
+    asm volatile("s_nop 1\n\tv_readfirstlane_b32 vcc_lo, %0\n\ts_cmp_eq_u32 vcc_lo, 0\n\ts_cbranch_scc1 0f\n\t"
                  "s_waitcnt vmcnt(%1)\n\ts_branch 1f\n0:\n\ts_waitcnt vmcnt(0)\n1:"
                  :
                  : "v"(some), "n"(SOME)
@@ -305,13 +312,12 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             const int from = (p.M & 127) == 0 ? begin & ~127 : begin;
             t.skip = begin - from;
             t.len = end > begin ? end - from : 0;
-            t.m0 = (int64_t)uniform(row) * BM;
-            t.n0 = (int64_t)uniform(col) * BN;
-            t.row_end = p.N;
-            t.out_row = (int64_t)t.g * p.N;
+            t.m0 = uniform(row) * BM;
+            t.n0 = uniform(col) * BN;
+            t.row_end = (int)p.N;
             t.a = descriptor(p.a, t.m0 * p.M + from, p.N * p.M);
             t.b = descriptor(p.b, t.n0 * p.M + from, p.K * p.M);
-            t.a_scale = t.b_scale = 0;
+            t.sa = t.sb = nullptr;
         } else {
             // tiles are numbered by group, then in patches
             t.g = uniform(s_groups.find(uniform(L / col_tiles), p.G));
@@ -319,18 +325,18 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             const int begin = end_of(last), end = t.g < 0 ? (int)p.M : end_of(t.g);
             const int first = last < 0 ? 0 : uniform(s_groups.upto[last]);
             patch(L - first * col_tiles, (end - begin + BM - 1) / BM, col_tiles, row, col);
-            t.m0 = begin + (int64_t)uniform(row) * BM;
-            t.n0 = (int64_t)uniform(col) * BN;
+            t.m0 = begin + uniform(row) * BM;
+            t.n0 = uniform(col) * BN;
             t.row_end = end;
-            t.out_row = 0;
             t.skip = 0;
             t.len = t.g < 0 ? 0 : (int)p.K;
             const int64_t e = max(t.g, 0);
             t.a = descriptor(p.a, t.m0 * p.K, p.M * p.K);
             t.b = descriptor(p.b, (e * p.N + t.n0) * p.K, p.G * p.N * p.K);
-            t.a_scale = t.m0 * nkb;
-            t.b_scale = (e * nnb + min((t.n0 + wn) / 128, nnb - 1)) * nkb;
+            t.sa = p.a_scales + t.m0 * nkb;
+            t.sb = p.b_scales + (e * nnb + min((int64_t)(t.n0 + wn) / 128, nnb - 1)) * nkb;
         }
+        t.steps = max((t.len + kBK - 1) / kBK, kMinSteps);
         return t;
     };
     int b = blockIdx.x;
@@ -345,36 +351,39 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     const uint32_t stride = (uint32_t)(WGRAD ? p.M : p.K);
     const uint32_t va = (wave * 8 + lrow) * stride + chunk_a * 16, vb = (wave * 8 + lrow) * stride + chunk_b * 16;
     const uint32_t lds_a = uniform((int)lds_address(s_a)), lds_b = uniform((int)lds_address(s_b));
-    auto start_loads = [&](const Tile& t, int k, int buf) {
-        load_tile<WAVES, BM>(t.a, va, stride, chunk_a, k * kBK, t.len, t.skip, lds_a + buf * (BM * kBK), wave);
-        load_tile<WAVES, BN>(t.b, vb, stride, chunk_b, k * kBK, t.len, t.skip, lds_b + buf * (BN * kBK), wave);
+    // step k of t, which is past its end where it is one of the next tile
+    auto start_loads = [&](const Tile& t, const Tile& next, int k, int buf) {
+        const bool over = k >= t.steps;
+        const int kk = (over ? k - t.steps : k) * kBK, len = over ? next.len : t.len, skip = over ? next.skip : t.skip;
+        const v4i a{over ? next.a[0] : t.a[0], over ? next.a[1] : t.a[1], over ? next.a[2] : t.a[2], t.a[3]};
+        const v4i b{over ? next.b[0] : t.b[0], over ? next.b[1] : t.b[1], over ? next.b[2] : t.b[2], t.b[3]};
+        load_tile<WAVES, BM>(a, va, stride, chunk_a, kk, len, skip, lds_a + buf * (BM * kBK), wave);
+        load_tile<WAVES, BN>(b, vb, stride, chunk_b, kk, len, skip, lds_b + buf * (BN * kBK), wave);
     };
-    // Scales come two steps ahead, in a ring of four: a step's loads are issued
-    // after the scales of the step behind it, so waiting for a scale never waits
-    // for a tile.
+    // block128: a thread fetches one row's scale, three steps ahead, and puts
+    // its reciprocal into a ring of four steps; the columns' scale comes one step
+    // ahead. A step's loads are issued after the scales of the step behind it, so
+    // waiting for a scale never waits for a tile.
     const int srow = threadIdx.x % BM;
-    uint32_t srow_at = 0;
-    float sa_0 = 1.0f, sa_1 = 1.0f, sa_next = 1.0f, sb_next = 1.0f;
-    auto row_scale = [&](const Tile& t, int k) {
-        return (p.a_scales + t.a_scale + k)[srow_at];
+    const int nkb32 = (int)nkb;
+    float sa_next = 1.0f, sb_next = 1.0f;
+    auto row_scale = [&](const Tile& t, const Tile& next, int k) {
+        const bool over = k >= t.steps;
+        const int at = min(over ? k - t.steps : k, nkb32 - 1), rows = (int)p.M - 1 - (over ? next.m0 : t.m0);
+        const float* s = (over ? next.sa : t.sa) + at;
+        return s[(uint32_t)min(srow, rows) * (uint32_t)nkb32];
     };
-    auto start_tile = [&](const Tile& t, int buf) {
-        if constexpr (WGRAD) {
-            const int x = threadIdx.x;          // one scale a thread
-            static_assert(!WGRAD || BM + BN <= WAVES * 64, "rows and columns");
-            const bool down = x < BM;
-            const int64_t at = down ? min(t.m0 + x, p.N - 1) : min(t.n0 + x - BM, p.K - 1);
-            sa_0 = (down ? p.a_scales : p.b_scales)[at * p.G + t.g];
-        } else if (t.len > 0) {
-            const int end = (t.len + kBK - 1) / kBK - 1;
-            srow_at = (uint32_t)min(srow, (int)(p.M - 1 - t.m0)) * (uint32_t)nkb;
-            sa_0 = row_scale(t, 0);
-            sa_1 = row_scale(t, min(1, end));
-            sa_next = row_scale(t, min(2, end));
-            sb_next = scalar_load(p.b_scales + t.b_scale);
-        }
-        start_loads(t, 0, buf);
-        start_loads(t, 1, buf ^ 1);
+    auto col_scale = [&](const Tile& t, const Tile& next, int k) {
+        const bool over = k >= t.steps;
+        return scalar_load((over ? next.sb : t.sb) + min(over ? k - t.steps : k, nkb32 - 1));
+    };
+    // wgrad: a thread fetches one scale of the tile's rows and columns
+    auto tile_scale = [&](const Tile& t) {
+        static_assert(!WGRAD || BM + BN <= WAVES * 64, "rows and columns");
+        const int x = threadIdx.x;
+        const bool down = x < BM;
+        const int64_t at = down ? min((int64_t)t.m0 + x, p.N - 1) : min((int64_t)t.n0 + x - BM, p.K - 1);
+        return (down ? p.a_scales : p.b_scales)[at * p.G + t.g];
     };
 
     // ---- fragments ----
@@ -390,12 +399,31 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     using Op = Operand<FAST>;
 
     Tile t = tile(b);
-    start_tile(t, 0);
+    if constexpr (WGRAD) {
+        sa_next = tile_scale(t);
+    } else {
+        s_scale[srow] = 1.0f / row_scale(t, t, 0);
+        s_scale[BM + srow] = 1.0f / row_scale(t, t, 1);
+        sa_next = row_scale(t, t, 2);
+        sb_next = col_scale(t, t, 0);
+    }
+    start_loads(t, t, 0, 0);
+    start_loads(t, t, 1, 1);
+    wait_some_or_none<LOADS>(1);
+    __syncthreads();
+    v8i fa = fragment(s_a[0] + a_at, lo, hi), fb[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fb[j] = fragment(s_b[0] + b_at + b_row(j) * kBK, lo, hi);
+
     int ring = 0;            // steps of the tiles before this one
     int parity = 0;          // of the tiles walked
-    int drain = 0;           // whether a tile's stores (and nothing else) follow this tile's first loads
+    int drain = 0;           // whether a tile's stores (and nothing else) follow the loads of this tile's second step
     for (;;) {
-    const int steps = (t.len + kBK - 1) / kBK;
+    const bool more = b + (int)gridDim.x < total;
+    Tile next = t;
+    next.len = 0;            // after the last tile, loads bring zeros
+    if (more) next = tile(b + gridDim.x);
+    const int steps = t.steps;
     v4f acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -403,18 +431,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
     float* const scale = s_scale + (WGRAD ? parity * (BM + BN) : 0);
     if constexpr (WGRAD) {
-        scale[threadIdx.x] = 1.0f / sa_0;
-    } else {
-        scale[(ring & 3) * BM + srow] = 1.0f / sa_0;
-        scale[((ring + 1) & 3) * BM + srow] = 1.0f / sa_1;
-    }
-    wait_some_or_none<STORES + LOADS>(drain);
-    __syncthreads();
-    v8i fa = {}, fb[NT] = {};
-    if (steps > 0) {
-        fa = fragment(s_a[ring & 1] + a_at, lo, hi);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) fb[j] = fragment(s_b[ring & 1] + b_at + b_row(j) * kBK, lo, hi);
+        scale[threadIdx.x] = 1.0f / sa_next;
+        sa_next = tile_scale(next);
     }
     // The scaled sums of a row's blocks are added while the next row's
     // instructions run.
@@ -432,9 +450,9 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     // before it is multiplied. The barrier stands before the last two rows,
     // whose fragments are already in registers: behind it the other buffer is
     // complete and this one free, so the loads of the step after next and the
-    // first fragments of the next step are on their way during the rest. Steps
-    // past the last one load zeros and are not computed; the body has no branch,
-    // which keeps each row's sums next to its instructions.
+    // first fragments of the next step are on their way during the rest; at a
+    // tile's end these are the next tile's. The body has no branch, which keeps
+    // each row's sums next to its instructions.
 #pragma clang loop unroll(disable)
     for (int k = 0; k < steps; ++k) {
         const int cur = (ring + k) & 1;
@@ -442,7 +460,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         float sb_inv = 0.0f;
         if constexpr (!WGRAD) {
             sb_inv = 1.0f / sb_next;
-            sb_next = scalar_load(p.b_scales + t.b_scale + min(k + 1, steps - 1));
+            sb_next = col_scale(t, next, k + 1);
         }
         auto multiply = [&](int i, const v8i& v) {
             const Op a(v);
@@ -479,13 +497,13 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             __builtin_amdgcn_sched_barrier(0);
         }
         // the next step's bytes are in LDS
-        wait_some_or_none<STORES>(k == 0 ? drain : 0);
+        wait_some_or_none<STORES + (WGRAD ? 1 : 0)>(k == 0 ? drain : 0);
         __syncthreads();
         if constexpr (!WGRAD) {
             scale[((ring + k + 2) & 3) * BM + srow] = 1.0f / sa_next;
-            sa_next = row_scale(t, min(k + 3, steps - 1));
+            sa_next = row_scale(t, next, k + 3);
         }
-        start_loads(t, k + 2, cur);
+        start_loads(t, next, k + 2, cur);
         multiply(MT - 2, fa);
         __builtin_amdgcn_sched_barrier(0);
         fa = fragment(na, lo, hi);
@@ -495,19 +513,12 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!WGRAD) promote(MT - 1);
-    ring += steps;
-
-    // Both buffers are free (every wave has read its last fragments before the
-    // last barrier): the next tile's first loads go out before the stores.
-    const Tile done = t;
-    b += gridDim.x;
-    const bool more = b < total;
-    if (more) {
-        t = tile(b);
-        start_tile(t, ring & 1);
+    if (t.len == 0) {        // whatever the scales of no rows are
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
     }
-    drain = p.accumulate ? 0 : 1;
-    parity ^= 1;
 
     // ---- store: 16 bytes a lane, whole 128-byte lines by eight lanes ----
     // A lane has two pieces of 16 bytes of a line: the first of lanes fr + 8 and
@@ -515,13 +526,14 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     // sixteen and the other rows 8-15. Stores outside the output are dropped by
     // the descriptor's bounds, so every tile issues the same number of them.
     const uint32_t pitch = (uint32_t)p.cols * (F32 ? 4 : 2);
-    const int64_t first = (done.out_row + done.m0) * pitch + done.n0 * (F32 ? 4 : 2);
-    const v4i out = descriptor(static_cast<uint8_t*>(p.out), first, (done.out_row + done.row_end) * pitch);
+    const int64_t row0 = WGRAD ? t.g * p.N : 0;
+    const v4i out = descriptor(static_cast<uint8_t*>(p.out), (row0 + t.m0) * pitch + t.n0 * (F32 ? 4 : 2),
+                               (row0 + t.row_end) * pitch);
     uint32_t at[NT / (F32 ? 2 : 4)];
 #pragma unroll
     for (int j = 0; j < NT / (F32 ? 2 : 4); ++j) {
         const int c = wn + (fg + (fr >> 3) * 4) * (F32 ? 4 : 8) + j * (F32 ? 32 : 64);
-        at[j] = done.n0 + c < p.cols ? (wm + (fr & 7)) * pitch + c * (F32 ? 4 : 2) : kOutOfRange;
+        at[j] = t.n0 + c < p.cols ? (wm + (fr & 7)) * pitch + c * (F32 ? 4 : 2) : kOutOfRange;
     }
     v4f ib[NT];
     if constexpr (WGRAD) {
@@ -561,8 +573,14 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             for (int h = 0; h < 2; ++h) store16(out, at[j] + (i * 16 + h * 8) * pitch, w[h], WGRAD && p.accumulate);
         }
     }
-    if (!more) return;
+    if (!more) break;
+    t = next;
+    b += gridDim.x;
+    ring += steps;
+    parity ^= 1;
+    drain = p.accumulate ? 0 : 1;
     }
+    load_wait();            // no load into LDS is left behind
 }
 
 template <int BM, int BN, int WM, int WN, bool WGRAD, bool FAST>
@@ -584,6 +602,7 @@ hipError_t launch(const MmArgs& p, bool f32, int64_t tiles, int cus, hipStream_t
 hipError_t launch_mm_block128(const uint8_t* a, const float* a_scales, int64_t M, int64_t K, const uint8_t* b,
                               const float* b_scales, int64_t E, int64_t N, const int32_t* offsets, bool fast,
                               bool f32, void* y, int cus, hipStream_t stream) {
+    if (K == 0) return launch_zero(y, (size_t)M * N * (f32 ? 4 : 2), stream);
     const MmArgs p{a, a_scales, b, b_scales, offsets, M, N, K, N, (int)E, 0, y};
     // every group, and the rows past the last one, may end inside a tile
     const int64_t tiles = M / 256 + (offsets ? E + 1 : 1);

@@ -88,6 +88,16 @@ __device__ __forceinline__ void load16_lds(v4i rsrc, uint32_t off, uint32_t lds)
 #endif
 }
 
+// 4 bytes a lane, likewise, into lds + 4 * lane.
+__device__ __forceinline__ void load4_lds(v4i rsrc, uint32_t off, uint32_t lds) {
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :
+                 : "v"(off), "s"(rsrc), "s"(lds)
+                 : "memory");
+#endif
+}
+
 // 16 bytes a lane to the descriptor's base + off, as output written once; with
 // `add`, added to the four binary32 values there.
 __device__ __forceinline__ void store16(v4i rsrc, uint32_t off, v4i v, bool add) {
@@ -277,8 +287,9 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     __shared__ __align__(128) uint8_t s_a[2][BM * kBK];
     __shared__ __align__(128) uint8_t s_b[2][BN * kBK];
     // block128: a ring of four steps' reciprocal scales of the rows; wgrad: the
-    // reciprocal scales of this and the next tile's rows and columns
-    __shared__ __align__(16) float s_scale[WGRAD ? 2 * (BM + BN) : 4 * BM];
+    // scales of the last, this and the next tile's rows and columns
+    __shared__ __align__(16) float s_scale[WGRAD ? 3 * (BM + BN) : 4 * BM];
+    __shared__ float s_raw[2][WGRAD ? 1 : WAVES * 64];     // block128: the scale each thread fetches, of two steps
     __shared__ Groups s_groups;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = uniform((int)(threadIdx.x / kWave));
@@ -360,30 +371,43 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         load_tile<WAVES, BM>(a, va, stride, chunk_a, kk, len, skip, lds_a + buf * (BM * kBK), wave);
         load_tile<WAVES, BN>(b, vb, stride, chunk_b, kk, len, skip, lds_b + buf * (BN * kBK), wave);
     };
-    // block128: a thread fetches one row's scale, three steps ahead, and puts
-    // its reciprocal into a ring of four steps; the columns' scale comes one step
-    // ahead. A step's loads are issued after the scales of the step behind it, so
-    // waiting for a scale never waits for a tile.
-    const int srow = threadIdx.x % BM;
+    // block128: a thread fetches one row's scale, three steps ahead, and puts its
+    // reciprocal into a ring of four steps when it has come; the columns' scale
+    // comes one step ahead through the scalar cache. wgrad: a thread fetches one
+    // scale of the next tile's rows and columns. Like the tiles, the scales come
+    // by loads that the compiler does not wait for: a wait for one of them alone
+    // would also be a wait for the stores before it.
+    int ring = 0;            // steps of the tiles before this one
     const int nkb32 = (int)nkb;
-    float sa_next = 1.0f, sb_next = 1.0f;
-    auto row_scale = [&](const Tile& t, const Tile& next, int k) {
+    const int srow = WGRAD ? (int)threadIdx.x % (BM + BN) : (int)threadIdx.x % BM;
+    const uint32_t lds_raw = uniform((int)lds_address(s_raw)) + wave * 256;
+    const uint32_t lds_scale = uniform((int)lds_address(s_scale)) + wave * 256;
+    const float *p_sa = p.a_scales, *p_sb = p.b_scales;
+    auto row_offset = [&](const Tile& t, const Tile& next, int k) {
+        const int rows = (int)p.M - 1 - (k >= t.steps ? next.m0 : t.m0);
+        return (uint32_t)min(srow, rows) * (uint32_t)nkb32;
+    };
+    auto row_scales = [&](const Tile& t, const Tile& next, int k) {
         const bool over = k >= t.steps;
-        const int at = min(over ? k - t.steps : k, nkb32 - 1), rows = (int)p.M - 1 - (over ? next.m0 : t.m0);
-        const float* s = (over ? next.sa : t.sa) + at;
-        return s[(uint32_t)min(srow, rows) * (uint32_t)nkb32];
+        return (over ? next.sa : t.sa) + min(over ? k - t.steps : k, nkb32 - 1);
     };
     auto col_scale = [&](const Tile& t, const Tile& next, int k) {
         const bool over = k >= t.steps;
         return scalar_load((over ? next.sb : t.sb) + min(over ? k - t.steps : k, nkb32 - 1));
     };
-    // wgrad: a thread fetches one scale of the tile's rows and columns
-    auto tile_scale = [&](const Tile& t) {
-        static_assert(!WGRAD || BM + BN <= WAVES * 64, "rows and columns");
-        const int x = threadIdx.x;
-        const bool down = x < BM;
-        const int64_t at = down ? min((int64_t)t.m0 + x, p.N - 1) : min((int64_t)t.n0 + x - BM, p.K - 1);
-        return (down ? p.a_scales : p.b_scales)[at * p.G + t.g];
+    auto start_scales = [&](const Tile& t, const Tile& next, int k) {
+        const float* s = row_scales(t, next, k);
+        load4_lds(descriptor(reinterpret_cast<const uint8_t*>(s), 0, 0x7FFFFFFF), row_offset(t, next, k) * 4,
+                  lds_raw + ((ring + k) & 1) * (WAVES * 256));
+    };
+    auto start_tile_scales = [&](const Tile& t, int third) {
+        static_assert(!WGRAD || BM + BN == WAVES * 64, "a thread fetches one scale");
+        const bool down = wave * 64 < BM;        // a wave's are all rows or all columns
+        const int64_t first = down ? t.m0 : t.n0;
+        const int at = min(down ? srow : srow - BM, (int)min((down ? p.N : p.K) - 1 - first, (int64_t)BM + BN));
+        const float* s = (down ? p_sa : p_sb) + first * p.G + t.g;
+        load4_lds(descriptor(reinterpret_cast<const uint8_t*>(s), 0, 0x7FFFFFFF), (uint32_t)at * (uint32_t)p.G * 4,
+                  lds_scale + third * (WAVES * 256));
     };
 
     // ---- fragments ----
@@ -400,13 +424,13 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
 
     Tile t = tile(b);
     if constexpr (WGRAD) {
-        sa_next = tile_scale(t);
+        start_tile_scales(t, 0);
     } else {
-        s_scale[srow] = 1.0f / row_scale(t, t, 0);
-        s_scale[BM + srow] = 1.0f / row_scale(t, t, 1);
-        sa_next = row_scale(t, t, 2);
-        sb_next = col_scale(t, t, 0);
+        s_scale[srow] = 1.0f / row_scales(t, t, 0)[row_offset(t, t, 0)];
+        s_scale[BM + srow] = 1.0f / row_scales(t, t, 1)[row_offset(t, t, 0)];
+        s_raw[0][threadIdx.x] = row_scales(t, t, 2)[row_offset(t, t, 0)];
     }
+    float sb_next = WGRAD ? 1.0f : col_scale(t, t, 0);
     start_loads(t, t, 0, 0);
     start_loads(t, t, 1, 1);
     wait_some_or_none<LOADS>(1);
@@ -415,8 +439,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
 #pragma unroll
     for (int j = 0; j < NT; ++j) fb[j] = fragment(s_b[0] + b_at + b_row(j) * kBK, lo, hi);
 
-    int ring = 0;            // steps of the tiles before this one
-    int parity = 0;          // of the tiles walked
+    int third = 0;           // of s_scale: tiles walked modulo 3
     int drain = 0;           // whether a tile's stores (and nothing else) follow the loads of this tile's second step
     for (;;) {
     const bool more = b + (int)gridDim.x < total;
@@ -429,11 +452,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-    float* const scale = s_scale + (WGRAD ? parity * (BM + BN) : 0);
-    if constexpr (WGRAD) {
-        scale[threadIdx.x] = 1.0f / sa_next;
-        sa_next = tile_scale(next);
-    }
+    float* const scale = s_scale + (WGRAD ? third * (BM + BN) : 0);
+    if constexpr (WGRAD) start_tile_scales(next, third == 2 ? 0 : third + 1);
     // The scaled sums of a row's blocks are added while the next row's
     // instructions run.
     v4f part[NT];
@@ -500,8 +520,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         wait_some_or_none<STORES + (WGRAD ? 1 : 0)>(k == 0 ? drain : 0);
         __syncthreads();
         if constexpr (!WGRAD) {
-            scale[((ring + k + 2) & 3) * BM + srow] = 1.0f / sa_next;
-            sa_next = row_scale(t, next, k + 3);
+            scale[((ring + k + 2) & 3) * BM + srow] = 1.0f / s_raw[(ring + k) & 1][threadIdx.x];
+            start_scales(t, next, k + 3);
         }
         start_loads(t, next, k + 2, cur);
         multiply(MT - 2, fa);
@@ -538,13 +558,16 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     v4f ib[NT];
     if constexpr (WGRAD) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j) {
             ib[j] = *reinterpret_cast<const v4f*>(scale + BM + wn + (F32 ? j * 16 + fg * 4 : (j >> 1) * 32 + fg * 8 + (j & 1) * 4));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ib[j][c] = 1.0f / ib[j][c];
+        }
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         if constexpr (WGRAD) {
-            const float ia = scale[wm + fr + i * 16];
+            const float ia = 1.0f / scale[wm + fr + i * 16];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -570,14 +593,14 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
                 w[1][c] = __builtin_amdgcn_update_dpp(v[1][c], v[0][c], 0x128, 0xF, 0x3, false);
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) store16(out, at[j] + (i * 16 + h * 8) * pitch, w[h], WGRAD && p.accumulate);
+            for (int h = 0; h < 2; ++h) store16(out, at[j] + (i * 16 + h * 8) * pitch, w[h], WGRAD && F32 && p.accumulate);
         }
     }
     if (!more) break;
     t = next;
     b += gridDim.x;
     ring += steps;
-    parity ^= 1;
+    third = third == 2 ? 0 : third + 1;
     drain = p.accumulate ? 0 : 1;
     }
     load_wait();            // no load into LDS is left behind

@@ -63,8 +63,10 @@ struct Tile {
     const float *sa, *sb;    // block128: scales of the first row and of the wave's columns
 };
 
-// Loads run two steps ahead of the sums and scales three, at most one tile on.
-constexpr int kMinSteps = 3;
+// Loads run two steps ahead of the sums, and block128's scales three, at most
+// one tile on: so many steps a tile has at least.
+template <bool WGRAD>
+constexpr int kMinSteps = WGRAD ? 2 : 3;
 
 // The buffer descriptor of the bytes from p + at to the end of an array of size
 // bytes: base, size, raw 32-bit data. Loads past the end give zeros.
@@ -167,23 +169,31 @@ struct Operand;
 template <>
 struct Operand<true> {
     v8i v;
+    __device__ __forceinline__ Operand() {}
     __device__ __forceinline__ explicit Operand(v8i x) : v(x) {}
-    __device__ __forceinline__ static v4f mfma(const Operand& a, const Operand& b, v4f c) {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, c, 0, 0, 0, 0, 0, 0);
+    // c[j] += a[j] b, instruction by instruction over the j
+    template <int N>
+    __device__ __forceinline__ static void mfma(const Operand (&a)[N], const Operand& b, v4f (&c)[N]) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            c[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j].v, b.v, c[j], 0, 0, 0, 0, 0, 0);
     }
 };
 
 template <>
 struct Operand<false> {
     v8b v[4];
+    __device__ __forceinline__ Operand() {}
     __device__ __forceinline__ explicit Operand(v8i x) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = widen(x[2 * i], x[2 * i + 1]);
     }
-    __device__ __forceinline__ static v4f mfma(const Operand& a, const Operand& b, v4f c) {
+    template <int N>
+    __device__ __forceinline__ static void mfma(const Operand (&a)[N], const Operand& b, v4f (&c)[N]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
-        return c;
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j].v[i], b.v[i], c[j], 0, 0, 0);
     }
 };
 
@@ -288,7 +298,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     __shared__ __align__(128) uint8_t s_b[2][BN * kBK];
     // block128: a ring of four steps' reciprocal scales of the rows; wgrad: the
     // scales of the last, this and the next tile's rows and columns
-    __shared__ __align__(16) float s_scale[WGRAD ? 3 * (BM + BN) : 4 * BM];
+    __shared__ __align__(16) float s_scale[WGRAD ? 3 * WAVES * 64 : 4 * BM];
     __shared__ float s_raw[2][WGRAD ? 1 : WAVES * 64];     // block128: the scale each thread fetches, of two steps
     __shared__ Groups s_groups;
     const int lane = threadIdx.x & (kWave - 1);
@@ -347,7 +357,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             t.sa = p.a_scales + t.m0 * nkb;
             t.sb = p.b_scales + (e * nnb + min((int64_t)(t.n0 + wn) / 128, nnb - 1)) * nkb;
         }
-        t.steps = max((t.len + kBK - 1) / kBK, kMinSteps);
+        t.steps = max((t.len + kBK - 1) / kBK, kMinSteps<WGRAD>);
         return t;
     };
     int b = blockIdx.x;
@@ -401,7 +411,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
                   lds_raw + ((ring + k) & 1) * (WAVES * 256));
     };
     auto start_tile_scales = [&](const Tile& t, int third) {
-        static_assert(!WGRAD || BM + BN == WAVES * 64, "a thread fetches one scale");
+        static_assert(!WGRAD || BM + BN <= WAVES * 64, "a thread fetches one scale");
         const bool down = wave * 64 < BM;        // a wave's are all rows or all columns
         const int64_t first = down ? t.m0 : t.n0;
         const int at = min(down ? srow : srow - BM, (int)min((down ? p.N : p.K) - 1 - first, (int64_t)BM + BN));
@@ -452,7 +462,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-    float* const scale = s_scale + (WGRAD ? third * (BM + BN) : 0);
+    float* const scale = s_scale + (WGRAD ? third * (WAVES * 64) : 0);
     if constexpr (WGRAD) start_tile_scales(next, third == 2 ? 0 : third + 1);
     // The scaled sums of a row's blocks are added while the next row's
     // instructions run.
@@ -482,25 +492,26 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             sb_inv = 1.0f / sb_next;
             sb_next = col_scale(t, next, k + 1);
         }
+        Op ob[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) ob[j] = Op(fb[j]);
         auto multiply = [&](int i, const v8i& v) {
             const Op a(v);
             if constexpr (WGRAD) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc[i][j] = Op::mfma(Op(fb[j]), a, acc[i][j]);
+                Op::mfma(ob, a, acc[i]);
             } else {
                 const float f = scale[((ring + k) & 3) * BM + wm + i * 16 + fr] * sb_inv;
                 v4f now[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) now[j] = Op::mfma(Op(fb[j]), a, v4f{0, 0, 0, 0});
+                for (int j = 0; j < NT; ++j) now[j] = v4f{0, 0, 0, 0};
+                Op::mfma(ob, a, now);
                 promote((i + MT - 1) % MT);
-                if constexpr (FAST) {
-                    // an instruction, then the additions of a sum that an
-                    // earlier one finished
+                // an instruction, then the additions of a sum that an earlier
+                // one finished
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
-                    }
+                for (int j = 0; j < NT * (FAST ? 1 : 4); ++j) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, FAST ? 5 : 3, 0);
                 }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) part[j] = now[j];
@@ -606,11 +617,187 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     load_wait();            // no load into LDS is left behind
 }
 
+// ---- block128 for few rows a group -------------------------------------------
+//
+// With a handful of rows the weights' bytes are the whole cost: a tile is BM
+// rows by 32 columns, and its eight waves take the contraction's blocks in turn
+// (wave w: w, w + 8, ...), so that even one small product has enough loads in
+// flight on every CU. Fragments come straight from memory, four lanes a line,
+// the next block's while this one is multiplied; sums are exact (the matrix
+// cores have nothing else to do). The waves' sums meet in LDS and are added in
+// wave order.
+constexpr int kFewCols = 32, kFewWaves = 8;
+
+// The 32 bytes at p, or zeros.
+__device__ __forceinline__ v8i load32(const uint8_t* p, bool some) {
+    v4i lo = *reinterpret_cast<const v4i*>(p), hi = *reinterpret_cast<const v4i*>(p + 16);
+    return some ? __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) : v8i{};
+}
+
+template <int BM, bool F32>
+__global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
+    constexpr int MT = BM / 16, NT = kFewCols / 16;
+    __shared__ __align__(16) float s_sum[kFewWaves][BM][kFewCols + 4];
+    const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)(threadIdx.x / kWave));
+    const int nkb = (int)((p.K + kBK - 1) / kBK);
+    const int64_t nnb = (p.N + 127) / 128;
+    const int col_tiles = (int)((p.N + kFewCols - 1) / kFewCols), M = (int)p.M;
+
+    // ---- which tile: every wave finds it, 64 groups at a time ----
+    int carry = 0, tiles = 0;
+    int e = 0, b = 0;                      // this lane's group
+    auto group = [&](int g, int from) {
+        int raw = 0;
+        if (g < p.G) raw = p.offsets ? min(max(p.offsets[g], 0), M) : M;
+        e = max(wave_prefix_imax(raw), from);
+        b = __shfl_up(e, 1, kWave);
+        if (lane == 0) b = from;
+        return wave_prefix_sum((e - b + BM - 1) / BM);
+    };
+    int upto = 0;
+    for (int base = 0; base < p.G; base += kWave) {
+        upto = tiles + group(base + lane, carry);
+        tiles = uniform(__shfl(upto, kWave - 1, kWave));
+        carry = uniform(__shfl(e, kWave - 1, kWave));
+    }
+    const int last_end = carry, total = (tiles + (M - last_end + BM - 1) / BM) * col_tiles;
+    if ((int)blockIdx.x >= total) return;
+    const int L = tile_of(blockIdx.x, total);
+    int g = -1, begin = last_end, end = M, before = tiles;
+    if (L < tiles * col_tiles) {
+        if (p.G > kWave) {
+            carry = tiles = 0;
+            for (int base = 0;; base += kWave) {
+                upto = tiles + group(base + lane, carry);
+                g = base;
+                const int now = uniform(__shfl(upto, kWave - 1, kWave));
+                if (L < now * col_tiles) break;
+                tiles = now;
+                carry = uniform(__shfl(e, kWave - 1, kWave));
+            }
+        } else {
+            g = 0;
+        }
+        const int at = __builtin_ctzll(__ballot(upto * col_tiles > L));
+        g = uniform(g + at);
+        begin = uniform(__shfl(b, at, kWave));
+        end = uniform(__shfl(e, at, kWave));
+        before = uniform(__shfl(upto, at, kWave)) - (end - begin + BM - 1) / BM;
+    }
+    const int rows = (end - begin + BM - 1) / BM, local = L - before * col_tiles;
+    const int m0 = begin + local % rows * BM, n0 = local / rows * kFewCols;
+
+    // ---- the contraction ----
+    const int fr = lane & 15, fg = lane / 16;
+    v4f acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+    if (g >= 0) {
+        const uint8_t *pa[MT], *pb[NT];
+        const float *psa[MT], *psb = p.b_scales + (g * nnb + n0 / 128) * nkb;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int64_t r = min(m0 + i * 16 + fr, end - 1);
+            pa[i] = p.a + r * p.K;
+            psa[i] = p.a_scales + r * nkb;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) pb[j] = p.b + (g * p.N + min((int64_t)n0 + j * 16 + fr, p.N - 1)) * p.K;
+        v8i fa[MT], fb[NT];
+        float sa[MT], sb;
+        auto fetch = [&](int k) {
+            // a lane's 32 bytes may end past the contraction (K is a multiple of
+            // 16): then it is read 16 bytes back, or not at all
+            const int64_t at = (int64_t)k * kBK + fg * 32;
+            const bool some = at < p.K, half = at + 32 > p.K;
+            const int64_t from = some ? (half ? at - 16 : at) : 0;
+            auto get = [&](const uint8_t* q) {
+                v8i v = load32(q + from, some);
+                if (half && some) v = v8i{v[4], v[5], v[6], v[7], 0, 0, 0, 0};
+                return v;
+            };
+#pragma unroll
+            for (int j = 0; j < NT; ++j) fb[j] = get(pb[j]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                fa[i] = get(pa[i]);
+                sa[i] = psa[i][k];
+            }
+            sb = psb[k];
+        };
+        if (wave < nkb) fetch(wave);
+        for (int k = wave; k < nkb; k += kFewWaves) {
+            v8i na[MT], nb[NT];
+            float f[MT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) nb[j] = fb[j];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                na[i] = fa[i];
+                f[i] = (1.0f / sa[i]) * (1.0f / sb);
+            }
+            if (k + kFewWaves < nkb) fetch(k + kFewWaves);
+            using Op = Operand<false>;
+            Op ob[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) ob[j] = Op(nb[j]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                v4f part[NT] = {};
+                Op::mfma(ob, Op(na[i]), part);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(part[j][c], f[i], acc[i][j][c]);
+            }
+        }
+    }
+
+    // ---- join and store ----
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<v4f*>(&s_sum[wave][i * 16 + fr][j * 16 + fg * 4]) = acc[i][j];
+    __syncthreads();
+    for (int x = threadIdx.x; x < BM * kFewCols / 4; x += kFewWaves * 64) {
+        const int r = x / (kFewCols / 4), c = x % (kFewCols / 4) * 4;
+        if (m0 + r >= end || n0 + c >= p.N) continue;
+        v4f v = *reinterpret_cast<const v4f*>(&s_sum[0][r][c]);
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) v += *reinterpret_cast<const v4f*>(&s_sum[w][r][c]);
+        const int64_t at = (int64_t)(m0 + r) * p.N + n0 + c;
+        if constexpr (F32)
+            *reinterpret_cast<v4f*>(static_cast<float*>(p.out) + at) = v;
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+    }
+}
+
+template <int BM>
+hipError_t launch_few(const MmArgs& p, bool f32, hipStream_t stream) {
+    const int64_t groups = p.offsets ? p.G + 1 : 1;
+    const int64_t blocks = (p.M + (groups < p.M ? groups : p.M) * (BM - 1)) / BM * ((p.N + kFewCols - 1) / kFewCols);
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (f32)
+        hipLaunchKernelGGL((mm_few_kernel<BM, true>), dim3((unsigned)blocks), dim3(kFewWaves * 64), 0, stream, p);
+    else
+        hipLaunchKernelGGL((mm_few_kernel<BM, false>), dim3((unsigned)blocks), dim3(kFewWaves * 64), 0, stream, p);
+    return hipGetLastError();
+}
+
 template <int BM, int BN, int WM, int WN, bool WGRAD, bool FAST>
-hipError_t launch(const MmArgs& p, bool f32, int64_t tiles, int cus, hipStream_t stream) {
+hipError_t launch(const MmArgs& p, bool f32, int cus, hipStream_t stream) {
     constexpr int threads = BM / WM * (BN / WN) * 64;
+    constexpr int per_cu = 512 / threads;        // workgroups of at most 256 registers a lane
+    // block128: every group, and the rows past the last one, may end inside a tile
+    const int64_t down = WGRAD ? p.G * ((p.N + BM - 1) / BM) : p.M / BM + (p.offsets ? p.G + 1 : 1);
+    const int64_t tiles = down * ((p.cols + BN - 1) / BN);
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    const int64_t blocks = tiles < cus ? tiles : cus;
+    const int64_t blocks = tiles < cus * per_cu ? tiles : cus * per_cu;
     if (f32)
         hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, WGRAD, FAST, true>), dim3((unsigned)blocks), dim3(threads), 0,
                            stream, p);
@@ -620,6 +807,42 @@ hipError_t launch(const MmArgs& p, bool f32, int64_t tiles, int cus, hipStream_t
     return hipGetLastError();
 }
 
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Which form a product takes, from the sizes the host knows (us, MI355X):
+// - few rows: up to 20 rows a group on average, one row of fragments (M = 1 by
+//   8192 x 8192: 17, against 66 on tiles of 128 x 128; more rows a group only
+//   where there is one group: 512 rows in 16 groups by 2048 x 4096 take 58, and
+//   33 on tiles); up to 40 rows two, and four where that is at most one
+//   workgroup a CU (64 rows by 8192 x 8192: 39 and 66; 256 rows by 4096 x 4096,
+//   two a CU: 36 and 32).
+// - 256 x 256 tiles where they fill the CUs, twice if groups end inside them
+//   (block128 16640 x 5120 x 8192 in 16 groups: 822, and 1005 with 128 x 128;
+//   2048 x 4096 x 4096, half the CUs: 66 and 48) and, for wgrad, where the contraction is long or the tiles are many
+//   (16640 x 8192 x 5120 in 16 groups: 839 and 948; 4096 x 2048 x 2048 in 8
+//   groups, four steps a tile: 40 and 32).
+// - 128 x 128 tiles otherwise, two workgroups a CU; block128 with binary32 sums
+//   has no registers for more (256 x 128: 1591 and 1491).
+template <bool WGRAD, bool FAST>
+hipError_t launch_sized(const MmArgs& p, bool f32, int cus, hipStream_t stream) {
+    const int64_t groups = p.offsets ? p.G : 1;
+    if constexpr (WGRAD) {
+        const int64_t tiles = groups * up(p.N, 256) * up(p.K, 256);
+        if (tiles >= cus && (p.M / groups >= 2048 || tiles >= 4 * cus))
+            return launch<256, 256, 128, 64, true, FAST>(p, f32, cus, stream);
+    } else {
+        const int64_t rows = up(p.M, groups);
+        if (rows <= 20) return launch_few<16>(p, f32, stream);
+        if (groups == 1 && rows <= 40) return launch_few<32>(p, f32, stream);
+        if (groups == 1 && up(p.M, 64) * up(p.N, kFewCols) <= cus) return launch_few<64>(p, f32, stream);
+        if constexpr (FAST) {
+            if ((up(p.M, 256) + groups / 2) * up(p.N, 256) >= (groups == 1 ? cus : 2 * cus))
+                return launch<256, 256, 128, 64, false, true>(p, f32, cus, stream);
+        }
+    }
+    return launch<128, 128, 64, 64, WGRAD, FAST>(p, f32, cus, stream);
+}
+
 }  // namespace
 
 hipError_t launch_mm_block128(const uint8_t* a, const float* a_scales, int64_t M, int64_t K, const uint8_t* b,
@@ -627,20 +850,14 @@ hipError_t launch_mm_block128(const uint8_t* a, const float* a_scales, int64_t M
                               bool f32, void* y, int cus, hipStream_t stream) {
     if (K == 0) return launch_zero(y, (size_t)M * N * (f32 ? 4 : 2), stream);
     const MmArgs p{a, a_scales, b, b_scales, offsets, M, N, K, N, (int)E, 0, y};
-    // every group, and the rows past the last one, may end inside a tile
-    const int64_t tiles = M / 256 + (offsets ? E + 1 : 1);
-    const int64_t blocks = tiles * ((N + 255) / 256);
-    return fast ? launch<256, 256, 128, 64, false, true>(p, f32, blocks, cus, stream)
-                : launch<256, 128, 64, 64, false, false>(p, f32, tiles * ((N + 127) / 128), cus, stream);
+    return fast ? launch_sized<false, true>(p, f32, cus, stream) : launch_sized<false, false>(p, f32, cus, stream);
 }
 
 hipError_t launch_mm_wgrad(const uint8_t* a_t, const float* a_scales_t, const uint8_t* b_t,
                            const float* b_scales_t, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
                            int64_t G, bool fast, bool f32, bool accumulate, void* dw, int cus, hipStream_t stream) {
     const MmArgs p{a_t, a_scales_t, b_t, b_scales_t, offsets, M, N, K, K, (int)G, accumulate ? 1 : 0, dw};
-    const int64_t blocks = G * ((N + 255) / 256) * ((K + 255) / 256);
-    return fast ? launch<256, 256, 128, 64, true, true>(p, f32, blocks, cus, stream)
-                : launch<256, 256, 128, 64, true, false>(p, f32, blocks, cus, stream);
+    return fast ? launch_sized<true, true>(p, f32, cus, stream) : launch_sized<true, false>(p, f32, cus, stream);
 }
 
 }  // namespace mgs

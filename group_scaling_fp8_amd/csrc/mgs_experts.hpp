@@ -22,7 +22,8 @@ struct DispatchArgs {
     uint16_t* xp;           // (P, D) bf16 or null
     uint8_t* q;             // (P, D) E4M3 or null
     float* scales;          // (P, ceil(D / 128))
-    int32_t* hist;          // workspace: slot counts (moe_superblocks, E), or null
+    int32_t* hist;          // workspace: slot counts (moe_runs, E), or null
+    bool wide;              // 16-byte stores of q (set by launch_dispatch)
 };
 
 // An upper bound on the rows that the experts' groups take (a multiple of align).
@@ -31,16 +32,16 @@ inline int64_t moe_rows_bound(int64_t n, int64_t E, int64_t align) {
     return (n + used * (align - 1)) / align * align;
 }
 
-// Slots up to this many are counted by every workgroup for itself. More are
-// first counted into the workspace, in at most 64 runs of moe_superblock slots.
-constexpr int64_t kMoeOneLaunchSlots = 8192;
-inline int64_t moe_superblock(int64_t n) {
+// Up to this many slots one launch does everything.
+constexpr int64_t kMoeFusedSlots = 512;
+// More are ranked in runs of moe_run slots, one workgroup each; counts of more
+// than one run go through the workspace (moe_runs, E).
+inline int64_t moe_run(int64_t n) {
     const int64_t s = (n + 63) / 64;
-    return s < 4096 ? 4096 : s;
+    return s < 8192 ? 8192 : s;
 }
-inline int64_t moe_superblocks(int64_t n) {
-    return n <= kMoeOneLaunchSlots ? 0 : (n + moe_superblock(n) - 1) / moe_superblock(n);
-}
+inline int64_t moe_runs(int64_t n) { return (n + moe_run(n) - 1) / moe_run(n); }
+inline int64_t moe_workspace(int64_t n, int64_t E) { return moe_runs(n) > 1 ? moe_runs(n) * E * 4 : 0; }
 
 hipError_t launch_dispatch(const DispatchArgs& a, int cus, hipStream_t stream);
 

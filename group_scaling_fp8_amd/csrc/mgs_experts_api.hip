@@ -42,7 +42,7 @@ int mgs_moe_workspace_bytes(int64_t T, int32_t top_k, int32_t n_experts, int64_t
     const int st = check_order(T, top_k, n_experts, 16);
     if (st != MGS_OK) return st;
     if (!bytes) return MGS_ERR_INVALID_ARG;
-    *bytes = mgs::moe_superblocks(T * top_k) * n_experts * (int64_t)sizeof(int32_t);
+    *bytes = mgs::moe_workspace(T * top_k, n_experts);
     return MGS_OK;
 }
 
@@ -63,13 +63,13 @@ int mgs_moe_dispatch(const void* x, int64_t T, int64_t D, const int32_t* expert_
     if ((q != nullptr) != (scales != nullptr)) return MGS_ERR_INVALID_ARG;
     if (moves && ((T > 0 && !x) || !aligned(x, 16) || !aligned(xp, 16) || !aligned(q, 8) || !aligned(scales, 4)))
         return MGS_ERR_INVALID_ARG;
-    const int64_t need = mgs::moe_superblocks(T * top_k) * n_experts * (int64_t)sizeof(int32_t);
+    const int64_t need = mgs::moe_workspace(T * top_k, n_experts);
     if (workspace_bytes < 0 || workspace_bytes < need || !aligned(workspace, 16) || (need > 0 && !workspace))
         return MGS_ERR_INVALID_ARG;
     const mgs::DispatchArgs a{static_cast<const uint16_t*>(x), expert_ids, T, moves ? D : 0, top_k, n_experts, align,
                               n_rows, (flags & MGS_FLAG_POW2_SCALE) ? 1 : 0, offsets, rows, slots,
                               moves ? static_cast<uint16_t*>(xp) : nullptr, moves ? static_cast<uint8_t*>(q) : nullptr,
-                              scales, static_cast<int32_t*>(workspace)};
+                              scales, static_cast<int32_t*>(workspace), false};
     return hip_status(mgs::launch_dispatch(a, mgs::device_cus(), as_stream(stream)));
 }
 

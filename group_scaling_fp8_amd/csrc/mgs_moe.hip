@@ -13,8 +13,42 @@ namespace mgs {
 
 namespace {
 
-constexpr int kDispatchThreads = 256;
-constexpr int kDispatchWaves = kDispatchThreads / kWave;
+// ---- the order ---------------------------------------------------------------
+//
+// Up to kMoeFusedSlots slots, every workgroup of the one dispatch kernel counts
+// all of them for itself. More are ranked first by rank_kernel, one workgroup of
+// 16 waves for each run of slots (with more than one run, hist_kernel counts
+// each run's slots before it), and dispatch reads rows and slots.
+
+// The lanes (of those with `held`) whose expert is this lane's: one ballot for
+// each bit of the id.
+__device__ __forceinline__ uint64_t same_expert(int e, bool held, int E) {
+    uint64_t same = __ballot(held);
+    for (int bit = 1; bit < E; bit <<= 1) {
+        const uint64_t set = __ballot(held && (e & bit));
+        same &= (e & bit) ? set : ~set;
+    }
+    return same;
+}
+
+__device__ __forceinline__ uint64_t lanes_below() {
+    return (1ull << (threadIdx.x & (kWave - 1))) - 1;
+}
+
+// First row of every expert's group from the slots of each, by one wave:
+// start[e] for e <= E.
+__device__ __forceinline__ void group_starts(const int* total, int* start, int E, int align) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int carry = 0;
+    for (int base = 0; base < E; base += kWave) {
+        const int e = base + lane;
+        const int full = e < E ? (total[e] + align - 1) / align * align : 0;
+        const int end = carry + wave_prefix_sum(full);
+        if (e < E) start[e] = end - full;
+        carry = __shfl(end, kWave - 1, kWave);
+    }
+    if (lane == 0) start[E] = carry;
+}
 
 __global__ __launch_bounds__(1024) void hist_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t run, int E,
                                                     int32_t* __restrict__ hist) {
@@ -30,141 +64,240 @@ __global__ __launch_bounds__(1024) void hist_kernel(const int32_t* __restrict__ 
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(int64_t)blockIdx.x * E + e] = s_hist[e];
 }
 
-// One row of padding: zeros and the scale of an empty block.
-__device__ __forceinline__ void zero_row(const DispatchArgs& a, int64_t p, int u0, int ustep, int units,
-                                         float empty_scale) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int64_t nb = (a.D + 127) / 128;
-    for (int u = u0; u < units; u += ustep) {
-        const int64_t col = (int64_t)u * 512 + lane * 8;
-        if (col < a.D) {
-            if (a.xp) *reinterpret_cast<uint4*>(a.xp + p * a.D + col) = make_uint4(0, 0, 0, 0);
-            if (a.q) {
-                *reinterpret_cast<uint2*>(a.q + p * a.D + col) = make_uint2(0, 0);
-                if ((lane & 15) == 0) a.scales[p * nb + col / 128] = empty_scale;
+// Rows of run blockIdx.x's slots. Wave w takes the run's w-th part: it counts
+// its slots of each expert, the counts are summed over the waves before it, and
+// it ranks its slots 64 at a time from there.
+__global__ __launch_bounds__(1024) void rank_kernel(DispatchArgs a, int64_t run) {
+    extern __shared__ int smem[];
+    const int threads = blockDim.x, waves = threads / kWave;
+    const int E = a.E, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    int* s_total = smem;                     // (E) slots of each expert
+    int* s_start = s_total + E;              // (E + 1) first row of each group
+    int* s_prior = s_start + E + 1;          // (E) slots of each expert in earlier runs
+    int* s_wave = s_prior + E;               // (waves, E) slots of each wave, then those before it
+    const int64_t n = a.T * a.k, lo = blockIdx.x * run, hi = min(lo + run, n);
+    const int64_t part = (run + waves - 1) / waves, first = min(lo + wave * part, hi), last = min(first + part, hi);
+    for (int i = tid; i < waves * E; i += threads) s_wave[i] = 0;
+    for (int e = tid; e < E; e += threads) s_total[e] = s_prior[e] = 0;
+    __syncthreads();
+    int* mine = s_wave + wave * E;
+    for (int64_t base = first; base < last; base += kWave) {
+        const int e = base + lane < last ? a.ids[base + lane] : -1;
+        const bool held = e >= 0 && e < E;
+        const uint64_t same = same_expert(e, held, E);
+        if (held && !(same & lanes_below())) mine[e] += __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += threads) {
+        int sum = 0;
+        for (int w = 0; w < waves; ++w) {
+            const int c = s_wave[w * E + e];
+            s_wave[w * E + e] = sum;
+            sum += c;
+        }
+        if (gridDim.x > 1) {
+            int all = 0, prior = 0;
+            for (int r = 0; r < (int)gridDim.x; ++r) {
+                const int c = a.hist[(int64_t)r * E + e];
+                if (r < (int)blockIdx.x) prior += c;
+                all += c;
             }
+            s_prior[e] = prior;
+            sum = all;
+        }
+        s_total[e] = sum;
+    }
+    __syncthreads();
+    if (wave == 0) group_starts(s_total, s_start, E, a.align);
+    __syncthreads();
+    for (int64_t base = first; base < last; base += kWave) {
+        const int64_t i = base + lane;
+        const int e = i < last ? a.ids[i] : -1;
+        const bool held = e >= 0 && e < E;
+        const uint64_t same = same_expert(e, held, E);
+        int row = -1;
+        if (held) row = s_start[e] + s_prior[e] + mine[e] + __popcll(same & lanes_below());
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (held && !(same & lanes_below())) mine[e] += __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (i < last) {
+            if (row >= a.P) row = -1;
+            a.rows[i] = row;
+            if (row >= 0) a.slots[row] = (int)i;
+        }
+    }
+    // offsets, and the rows that no slot takes
+    const int step = gridDim.x * threads, at = blockIdx.x * threads + tid;
+    for (int e = at; e < E; e += step) a.offsets[e] = s_start[e + 1];
+    for (int i = at; i < E * a.align; i += step) {
+        const int e = i / a.align, p = s_start[e] + s_total[e] + i - e * a.align;
+        if (p < s_start[e + 1]) a.slots[p] = -1;
+    }
+    for (int64_t p = (int64_t)s_start[E] + at; p < a.P; p += step) a.slots[p] = -1;
+}
+
+// ---- copy and cast -------------------------------------------------------------
+
+constexpr int kDispatchThreads = 256;
+constexpr int kDispatchWaves = kDispatchThreads / kWave;
+constexpr int kUnit = 1024;              // columns of a wave's piece: 16 a lane, eight lanes a block of 128
+
+// Max over groups of eight lanes, in every lane of them.
+__device__ __forceinline__ uint32_t row8_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));     // lane ^ 1
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));     // lane ^ 2
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));    // 7 - lane
+    return v;
+}
+
+// 16 columns of row p: `half` when only the first eight exist. Rows whose
+// length is an odd multiple of 8 are not 16-byte aligned.
+__device__ __forceinline__ void put(const DispatchArgs& a, int64_t p, int64_t col, bool half, const uint4 (&x)[2],
+                                    uint4 q, float scale) {
+    if (a.xp) {
+        uint4* o = reinterpret_cast<uint4*>(a.xp + p * a.D + col);
+        o[0] = x[0];
+        if (!half) o[1] = x[1];
+    }
+    if (a.q) {
+        uint8_t* o = a.q + p * a.D + col;
+        if (a.wide) {
+            *reinterpret_cast<uint4*>(o) = q;
+        } else {
+            reinterpret_cast<uint2*>(o)[0] = make_uint2(q.x, q.y);
+            if (!half) reinterpret_cast<uint2*>(o)[1] = make_uint2(q.z, q.w);
+        }
+        if ((threadIdx.x & 7) == 0) a.scales[p * ((a.D + 127) / 128) + col / 128] = scale;
+    }
+}
+
+// The units u0, u0 + ustep, ... of a row that no slot takes: zeros and the
+// scale of an empty block.
+__device__ __forceinline__ void zero_row(const DispatchArgs& a, int64_t p, int u0, int ustep, int units) {
+    const float scale = group_scale(0u, a.pow2 != 0);
+    const uint4 zero[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    for (int u = u0; u < units; u += ustep) {
+        const int64_t col = (int64_t)u * kUnit + (threadIdx.x & (kWave - 1)) * 16;
+        if (col < a.D) put(a, p, col, col + 8 >= a.D, zero, zero[0], scale);
+    }
+}
+
+// Units u0, u0 + ustep, ... of token t, cast once and written to the rows of its
+// k slots; U units' loads are under way at a time.
+template <int U>
+__device__ __forceinline__ void put_token(const DispatchArgs& a, int64_t t, const int* rows, int u0, int ustep, int units) {
+    const int lane = threadIdx.x & (kWave - 1);
+    for (int u = u0; u < units; u += U * ustep) {
+        uint4 x[U][2];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t col = (int64_t)(u + i * ustep) * kUnit + lane * 16;
+            const uint16_t* src = a.x + t * a.D + col;
+            x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+            if (u + i * ustep < units && col < a.D) x[i][0] = load_stream(src);
+            if (u + i * ustep < units && col + 8 < a.D) x[i][1] = load_stream(src + 8);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t col = (int64_t)(u + i * ustep) * kUnit + lane * 16;
+            const float s = group_scale(row8_max(mag_fold(mag_max8(mag_max8(0u, x[i][0]), x[i][1]))), a.pow2 != 0);
+            const uint2 lo = cast8_group(x[i][0], s), hi = cast8_group(x[i][1], s);
+            if (u + i * ustep < units && col < a.D)
+                for (int j = 0; j < a.k; ++j)
+                    if (rows[j] >= 0) put(a, rows[j], col, col + 8 >= a.D, x[i], make_uint4(lo.x, lo.y, hi.x, hi.y), s);
         }
     }
 }
 
-// Workgroup (b, c): tokens b * tb .. of the columns c, c + CS, ... in units of
-// 512. Every workgroup finds the row of each of its slots by itself.
-__global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs a, int tb, int64_t run, int runs) {
+// Everything in one launch, for few slots: workgroups below `tokens` take one
+// token each, all take a share of the rows without a slot, and grid.y splits the
+// columns. Every workgroup finds the order by itself.
+__global__ __launch_bounds__(kDispatchThreads) void dispatch_fused_kernel(DispatchArgs a, int tokens) {
     extern __shared__ int smem[];
-    int* s_total = smem;                // (E) slots of each expert
-    int* s_next = smem + a.E;           // (E) next row of each expert
-    int* s_start = smem + 2 * a.E;      // (E + 1) first row of each expert's group
-    int* s_row = smem + 3 * a.E + 1;    // (tb * k) rows of this workgroup's slots
     const int E = a.E, k = a.k, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    const int64_t t0 = (int64_t)blockIdx.x * tb, t1 = min(t0 + tb, a.T);
-    const int64_t n = a.T * k, first = t0 * k, last = t1 * k;
-    for (int e = tid; e < E; e += kDispatchThreads) s_total[e] = s_next[e] = 0;
+    int* s_total = smem;                // (E) slots of each expert
+    int* s_before = s_total + E;        // (E) those before this workgroup's token
+    int* s_start = s_before + E;        // (E + 1) first row of each group
+    int* s_row = s_start + E + 1;       // (k) rows of this workgroup's token
+    const int64_t t = blockIdx.x, n = a.T * k, first = min(t * k, n);
+    for (int e = tid; e < E; e += kDispatchThreads) s_total[e] = s_before[e] = 0;
     __syncthreads();
-    if (runs == 0) {
-        for (int64_t i = tid; i < n; i += kDispatchThreads) {
-            const int e = a.ids[i];
-            if (e >= 0 && e < E) {
-                atomicAdd(&s_total[e], 1);
-                if (i < first) atomicAdd(&s_next[e], 1);
-            }
-        }
-    } else {
-        const int mine = (int)(first / run);
-        for (int i = tid; i < runs * E; i += kDispatchThreads) {
-            const int j = i / E, e = i - j * E, v = a.hist[i];
-            atomicAdd(&s_total[e], v);
-            if (j < mine) atomicAdd(&s_next[e], v);
-        }
-        for (int64_t i = mine * run + tid; i < first; i += kDispatchThreads) {
-            const int e = a.ids[i];
-            if (e >= 0 && e < E) atomicAdd(&s_next[e], 1);
+    for (int64_t i = tid; i < n; i += kDispatchThreads) {
+        const int e = a.ids[i];
+        if (e >= 0 && e < E) {
+            atomicAdd(&s_total[e], 1);
+            if (i < first) atomicAdd(&s_before[e], 1);
         }
     }
     __syncthreads();
     if (wave == 0) {
-        int carry = 0;
-        for (int base = 0; base < E; base += kWave) {
-            const int e = base + lane;
-            const int full = e < E ? (s_total[e] + a.align - 1) / a.align * a.align : 0;
-            const int end = carry + wave_prefix_sum(full);
-            if (e < E) {
-                s_start[e] = end - full;
-                s_next[e] += end - full;
-            }
-            carry = __shfl(end, kWave - 1, kWave);
-        }
-        if (lane == 0) s_start[E] = carry;
+        group_starts(s_total, s_start, E, a.align);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-        // ranks in slot order, 64 slots at a time: lanes of the same expert
-        // find each other with one ballot for each bit of the id
-        for (int64_t base = first; base < last; base += kWave) {
-            const int64_t i = base + lane;
-            const int e = i < last ? a.ids[i] : -1;
+        if (t < tokens) {               // k is at most one wave's lanes
+            const int e = lane < k ? a.ids[first + lane] : -1;
             const bool held = e >= 0 && e < E;
-            uint64_t same = __ballot(held);
-            for (int bit = 1; bit < E; bit <<= 1) {
-                const uint64_t set = __ballot(held && (e & bit));
-                same &= (e & bit) ? set : ~set;
-            }
-            const int rank = __popcll(same & ((1ull << lane) - 1));
+            const uint64_t same = same_expert(e, held, E);
             int row = -1;
-            if (held) row = s_next[e] + rank;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (held && rank == 0) s_next[e] = row + __popcll(same);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (i < last) {
-                if (row >= a.P) row = -1;
-                s_row[i - first] = row;
+            if (held) row = s_start[e] + s_before[e] + __popcll(same & lanes_below());
+            if (row >= a.P) row = -1;
+            if (lane < k) {
+                s_row[lane] = row;
                 if (blockIdx.y == 0) {
-                    a.rows[i] = row;
-                    if (row >= 0) a.slots[row] = (int)i;
+                    a.rows[first + lane] = row;
+                    if (row >= 0) a.slots[row] = (int)(first + lane);
                 }
             }
         }
     }
     __syncthreads();
-    if (blockIdx.x == 0 && blockIdx.y == 0)
+    const int units = (int)((a.D + kUnit - 1) / kUnit), u0 = blockIdx.y;
+    if (blockIdx.x == 0 && u0 == 0)
         for (int e = tid; e < E; e += kDispatchThreads) a.offsets[e] = s_start[e + 1];
 
-    const int units = a.x ? (int)((a.D + 511) / 512) : 0;
-    const int CS = gridDim.y, own_units = units > (int)blockIdx.y ? (units - blockIdx.y + CS - 1) / CS : 0;
-    const int64_t nb = (a.D + 127) / 128;
-    const bool pow2 = a.pow2 != 0;
-
-    // padding rows: the end of each expert's group, and the rows past the last group
-    const float empty_scale = group_scale(0u, pow2);
-    for (int e = blockIdx.x * kDispatchWaves + wave; e < E; e += gridDim.x * kDispatchWaves) {
-        for (int64_t p = s_start[e] + s_total[e]; p < s_start[e + 1]; ++p) {
-            if (blockIdx.y == 0 && lane == 0) a.slots[p] = -1;
-            zero_row(a, p, blockIdx.y, CS, units, empty_scale);
+    // rows without a slot: place r of every group, dealt out over all waves
+    const int waves = gridDim.x * kDispatchWaves, w = blockIdx.x * kDispatchWaves + wave;
+    const int places = E * a.align, tail = (int)(a.P - s_start[E]);
+    for (int base = w; base < places + tail; base += waves * kWave) {
+        const int i = base + lane * waves;
+        int p = -1;
+        if (i < places) {
+            const int e = i / a.align;
+            p = s_start[e] + s_total[e] + i - e * a.align;
+            if (p >= s_start[e + 1]) p = -1;
+        } else if (i < places + tail) {
+            p = s_start[E] + i - places;
+        }
+        for (uint64_t left = __ballot(p >= 0); left; left &= left - 1) {
+            const int row = __shfl(p, __builtin_ctzll(left), kWave);
+            if (u0 == 0 && lane == 0) a.slots[row] = -1;
+            zero_row(a, row, u0, gridDim.y, units);
         }
     }
-    for (int64_t p = s_start[E] + (int64_t)blockIdx.x * kDispatchWaves + wave; p < a.P;
-         p += (int64_t)gridDim.x * kDispatchWaves) {
-        if (blockIdx.y == 0 && lane == 0) a.slots[p] = -1;
-        zero_row(a, p, blockIdx.y, CS, units, empty_scale);
-    }
+    if (t < tokens) put_token<1>(a, t, s_row, u0 + wave * gridDim.y, kDispatchWaves * gridDim.y, units);
+}
 
-    // each token is read and cast once and written to its k rows
-    const int items = (int)(t1 - t0) * own_units;
-    for (int it = wave; it < items; it += kDispatchWaves) {
-        const int t = it / own_units, u = blockIdx.y + (it - t * own_units) * CS;
-        const int64_t col = (int64_t)u * 512 + lane * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (col < a.D) v = load_stream(a.x + (t0 + t) * a.D + col);
-        const float s = group_scale(row16_max(mag_fold(mag_max8(0u, v))), pow2);
-        const uint2 c = cast8_group(v, s);
-        if (col < a.D) {
-            for (int j = 0; j < k; ++j) {
-                const int64_t p = s_row[t * k + j];
-                if (p < 0) continue;
-                if (a.xp) *reinterpret_cast<uint4*>(a.xp + p * a.D + col) = v;
-                if (a.q) {
-                    *reinterpret_cast<uint2*>(a.q + p * a.D + col) = c;
-                    if ((lane & 15) == 0) a.scales[p * nb + col / 128] = s;
-                }
-            }
+// Copy and cast by a known order: workgroups below `tokens` take one token each,
+// the others 64 rows each and zero those without a slot.
+template <int U>
+__global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs a, int tokens) {
+    __shared__ int s_row[kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int units = (int)((a.D + kUnit - 1) / kUnit);
+    const int64_t t = blockIdx.x;
+    if (t < tokens) {
+        if ((int)threadIdx.x < a.k) {
+            const int p = a.rows[t * a.k + threadIdx.x];
+            s_row[threadIdx.x] = p;
         }
+        __syncthreads();
+        put_token<U>(a, t, s_row, wave, kDispatchWaves, units);
+    } else {
+        const int64_t lo = (t - tokens) * kWave, p = lo + lane;
+        const int slot = p < a.P ? a.slots[p] : 0;
+        int turn = 0;
+        for (uint64_t left = __ballot(slot < 0); left; left &= left - 1, ++turn)
+            if (turn % kDispatchWaves == wave) zero_row(a, lo + __builtin_ctzll(left), 0, 1, units);
     }
 }
 
@@ -188,8 +321,9 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
     }
 }
 
-// Workgroups below T: dyp[rows[t, s]] = w[t, s] * dy[t] and
-// dw[t, s] = <dy[t], yp[rows[t, s]]>; the others zero the padding rows.
+// Workgroups (t, y) with t below T take the slots y, y + grid.y, ... of token t:
+// dyp[rows[t, s]] = w[t, s] * dy[t] and dw[t, s] = <dy[t], yp[rows[t, s]]>; the
+// others zero the rows without a slot.
 __global__ __launch_bounds__(256) void combine_grad_kernel(
         const uint16_t* __restrict__ dy, const uint16_t* __restrict__ yp, int64_t P, int64_t D,
         const int32_t* __restrict__ rows, const int32_t* __restrict__ slots, int64_t T, int k,
@@ -198,17 +332,19 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int64_t t = blockIdx.x;
     if (t >= T) {
-        const int64_t n = T * k;
-        const int64_t lo = (t - T) * 64, hi = min(lo + 64, P);
-        for (int64_t p = lo + wave; p < hi; p += 4) {
-            const int slot = slots[p];
-            if (slot >= 0 && slot < n) continue;
+        if (blockIdx.y > 0) return;
+        const int64_t n = T * k, lo = (t - T) * kWave, p = lo + lane;
+        const int slot = p < P ? slots[p] : 0;
+        int turn = 0;
+        for (uint64_t left = __ballot(p < P && (slot < 0 || slot >= n)); left; left &= left - 1, ++turn) {
+            if (turn % 4 != wave) continue;
+            uint16_t* row = dyp + (lo + __builtin_ctzll(left)) * D;
             for (int64_t col = lane * 8; col < D; col += 512)
-                *reinterpret_cast<uint4*>(dyp + p * D + col) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(row + col) = make_uint4(0, 0, 0, 0);
         }
         return;
     }
-    for (int s = 0; s < k; ++s) {
+    for (int s = blockIdx.y; s < k; s += gridDim.y) {
         const int64_t p = rows[t * k + s];
         float dot = 0.0f;
         if (p >= 0 && p < P) {
@@ -225,33 +361,46 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(
         if (lane == 0) s_part[s][wave] = dot;
     }
     __syncthreads();
-    if (threadIdx.x < k) {
-        const int s = threadIdx.x;
-        dw[t * k + s] = (s_part[s][0] + s_part[s][1]) + (s_part[s][2] + s_part[s][3]);
-    }
+    const int s = blockIdx.y + threadIdx.x * gridDim.y;
+    if (s < k) dw[t * k + s] = (s_part[s][0] + s_part[s][1]) + (s_part[s][2] + s_part[s][3]);
 }
 
 }  // namespace
 
-hipError_t launch_dispatch(const DispatchArgs& a, int cus, hipStream_t stream) {
-    const int64_t n = a.T * a.k;
-    const int64_t runs = moe_superblocks(n), run = moe_superblock(n);
-    if (runs > 0) {
-        hipLaunchKernelGGL(hist_kernel, dim3((unsigned)runs), dim3(1024), a.E * sizeof(int), stream, a.ids, n,
-                           run, a.E, a.hist);
+hipError_t launch_dispatch(const DispatchArgs& args, int cus, hipStream_t stream) {
+    DispatchArgs a = args;
+    a.wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
+    const int64_t n = a.T * a.k, units = (a.D + kUnit - 1) / kUnit;
+    const bool moves = a.xp || a.q;
+    if (n <= kMoeFusedSlots) {
+        // enough workgroups that a wave has about one row to zero
+        const int64_t spare = (a.P - n + kDispatchWaves - 1) / kDispatchWaves;
+        int64_t blocks = spare < cus ? spare : cus;
+        blocks = blocks > a.T ? blocks : a.T;
+        const size_t shmem = (3 * (size_t)a.E + 1 + kWave) * sizeof(int);
+        int64_t split = cus / (blocks > 0 ? blocks : 1);
+        split = split < 1 ? 1 : split > units ? (units > 0 ? units : 1) : split;
+        hipLaunchKernelGGL(dispatch_fused_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1), (unsigned)split),
+                           dim3(kDispatchThreads), shmem, stream, a, (int)a.T);
+        return hipGetLastError();
+    }
+    const int64_t runs = moe_runs(n), run = moe_run(n);
+    if (runs > 1) {
+        hipLaunchKernelGGL(hist_kernel, dim3((unsigned)runs), dim3(1024), a.E * sizeof(int), stream, a.ids, n, run,
+                           a.E, a.hist);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    // about four workgroups per CU before a workgroup takes more than one token
-    int64_t tb = a.T / (4 * (int64_t)cus);
-    tb = tb < 1 ? 1 : tb > 16 ? 16 : tb;
-    const int64_t blocks = a.T > 0 ? (a.T + tb - 1) / tb : 1;
-    const int64_t units = a.x ? (a.D + 511) / 512 : 1;
-    int64_t cs = 2 * (int64_t)cus / blocks;
-    cs = cs < 1 ? 1 : cs > (units + 3) / 4 ? (units + 3) / 4 : cs;
-    const size_t shmem = (3 * (size_t)a.E + 1 + (size_t)tb * a.k) * sizeof(int);
-    hipLaunchKernelGGL(dispatch_kernel, dim3((unsigned)blocks, (unsigned)cs), dim3(kDispatchThreads), shmem, stream,
-                       a, (int)tb, run, (int)runs);
+    const int waves = a.E > 512 ? 8 : 16;        // their counts take at most 32 KiB of LDS
+    const size_t shmem = (3 * (size_t)a.E + 1 + (size_t)waves * a.E) * sizeof(int);
+    hipLaunchKernelGGL(rank_kernel, dim3((unsigned)runs), dim3(waves * kWave), shmem, stream, a, run);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !moves) return e;
+    const int64_t blocks = a.T + (a.P + kWave - 1) / kWave;
+    if (units > kDispatchWaves)
+        hipLaunchKernelGGL(dispatch_kernel<2>, dim3((unsigned)blocks), dim3(kDispatchThreads), 0, stream, a, (int)a.T);
+    else
+        hipLaunchKernelGGL(dispatch_kernel<1>, dim3((unsigned)blocks), dim3(kDispatchThreads), 0, stream, a, (int)a.T);
     return hipGetLastError();
 }
 
@@ -265,9 +414,11 @@ hipError_t launch_combine(const uint16_t* yp, int64_t P, int64_t D, const int32_
 
 hipError_t launch_combine_grad(const uint16_t* dy, const uint16_t* yp, int64_t P, int64_t D,
                                const int32_t* rows, const int32_t* slots, int64_t T, int k,
-                               const float* weights, uint16_t* dyp, float* dw, int, hipStream_t stream) {
+                               const float* weights, uint16_t* dyp, float* dw, int cus, hipStream_t stream) {
     const int64_t blocks = T + (P + 63) / 64;
-    hipLaunchKernelGGL(combine_grad_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, dy, yp, P, D, rows, slots,
+    // few tokens: a workgroup for each slot instead of each token
+    const int64_t split = T < 4 * (int64_t)cus ? k : 1;
+    hipLaunchKernelGGL(combine_grad_kernel, dim3((unsigned)blocks, (unsigned)split), dim3(256), 0, stream, dy, yp, P, D, rows, slots,
                        T, k, weights, dyp, dw);
     return hipGetLastError();
 }

@@ -64,71 +64,89 @@ __global__ __launch_bounds__(1024) void hist_kernel(const int32_t* __restrict__ 
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[(int64_t)blockIdx.x * E + e] = s_hist[e];
 }
 
-// Rows of run blockIdx.x's slots. Wave w takes the run's w-th part: it counts
-// its slots of each expert, the counts are summed over the waves before it, and
-// it ranks its slots 64 at a time from there.
-__global__ __launch_bounds__(1024) void rank_kernel(DispatchArgs a, int64_t run) {
+// Rows of run blockIdx.x's slots. Wave w takes the run's w-th part and ranks its
+// slots among themselves, 64 at a time; then its counts are summed over the runs
+// and waves before it.
+template <int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void rank_kernel(DispatchArgs a, int64_t run) {
     extern __shared__ int smem[];
-    const int threads = blockDim.x, waves = threads / kWave;
     const int E = a.E, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     int* s_total = smem;                     // (E) slots of each expert
     int* s_start = s_total + E;              // (E + 1) first row of each group
-    int* s_prior = s_start + E + 1;          // (E) slots of each expert in earlier runs
-    int* s_wave = s_prior + E;               // (waves, E) slots of each wave, then those before it
+    int* s_wave = s_start + E + 1;           // (waves, E) slots of each wave, then the row its first one takes
     const int64_t n = a.T * a.k, lo = blockIdx.x * run, hi = min(lo + run, n);
-    const int64_t part = (run + waves - 1) / waves, first = min(lo + wave * part, hi), last = min(first + part, hi);
-    for (int i = tid; i < waves * E; i += threads) s_wave[i] = 0;
-    for (int e = tid; e < E; e += threads) s_total[e] = s_prior[e] = 0;
-    __syncthreads();
+    const int64_t part = (run + WAVES - 1) / WAVES, first = min(lo + wave * part, hi), last = min(first + part, hi);
     int* mine = s_wave + wave * E;
-    for (int64_t base = first; base < last; base += kWave) {
-        const int e = base + lane < last ? a.ids[base + lane] : -1;
-        const bool held = e >= 0 && e < E;
-        const uint64_t same = same_expert(e, held, E);
-        if (held && !(same & lanes_below())) mine[e] += __popcll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int e = lane; e < E; e += kWave) mine[e] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // place[c]: how many slots of its expert come before the lane's, in its wave
+    constexpr int C = 8;        // 8 x 64 slots at a time
+    int id[C], place[C];
+    const bool once = last - first <= C * kWave;      // they stay in registers, else in rows
+    for (int64_t base = first; base < last; base += C * kWave) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t i = base + c * kWave + lane;
+            id[c] = i < last ? a.ids[i] : -1;
+        }
+        uint64_t same[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) same[c] = same_expert(id[c], id[c] >= 0 && id[c] < E, E);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = id[c], below = __popcll(same[c] & lanes_below());
+            const bool held = e >= 0 && e < E;
+            place[c] = held ? mine[e] + below : -1;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (held && below == 0) mine[e] = place[c] + __popcll(same[c]);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+        if (!once) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int64_t i = base + c * kWave + lane;
+                if (i < last) a.rows[i] = place[c];
+            }
+        }
     }
     __syncthreads();
-    for (int e = tid; e < E; e += threads) {
-        int sum = 0;
-        for (int w = 0; w < waves; ++w) {
-            const int c = s_wave[w * E + e];
-            s_wave[w * E + e] = sum;
-            sum += c;
-        }
+    for (int e = tid; e < E; e += WAVES * 64) {
+        int count[WAVES], sum = 0, prior = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) count[w] = s_wave[w * E + e];
         if (gridDim.x > 1) {
-            int all = 0, prior = 0;
             for (int r = 0; r < (int)gridDim.x; ++r) {
                 const int c = a.hist[(int64_t)r * E + e];
                 if (r < (int)blockIdx.x) prior += c;
-                all += c;
+                sum += c;
             }
-            s_prior[e] = prior;
-            sum = all;
         }
-        s_total[e] = sum;
+        int before = prior;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            s_wave[w * E + e] = before;
+            before += count[w];
+        }
+        s_total[e] = gridDim.x > 1 ? sum : before;
     }
     __syncthreads();
     if (wave == 0) group_starts(s_total, s_start, E, a.align);
     __syncthreads();
-    for (int64_t base = first; base < last; base += kWave) {
-        const int64_t i = base + lane;
-        const int e = i < last ? a.ids[i] : -1;
-        const bool held = e >= 0 && e < E;
-        const uint64_t same = same_expert(e, held, E);
-        int row = -1;
-        if (held) row = s_start[e] + s_prior[e] + mine[e] + __popcll(same & lanes_below());
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (held && !(same & lanes_below())) mine[e] += __popcll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (i < last) {
+    for (int64_t base = first; base < last; base += C * kWave) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t i = base + c * kWave + lane;
+            if (i >= last) continue;
+            const int e = once ? id[c] : a.ids[i];
+            int row = once ? place[c] : a.rows[i];
+            if (row >= 0) row += s_start[e] + mine[e];
             if (row >= a.P) row = -1;
             a.rows[i] = row;
             if (row >= 0) a.slots[row] = (int)i;
         }
     }
     // offsets, and the rows that no slot takes
-    const int step = gridDim.x * threads, at = blockIdx.x * threads + tid;
+    const int step = gridDim.x * WAVES * 64, at = blockIdx.x * WAVES * 64 + tid;
     for (int e = at; e < E; e += step) a.offsets[e] = s_start[e + 1];
     for (int i = at; i < E * a.align; i += step) {
         const int e = i / a.align, p = s_start[e] + s_total[e] + i - e * a.align;
@@ -156,17 +174,17 @@ __device__ __forceinline__ uint32_t row8_max(uint32_t v) {
 __device__ __forceinline__ void put(const DispatchArgs& a, int64_t p, int64_t col, bool half, const uint4 (&x)[2],
                                     uint4 q, float scale) {
     if (a.xp) {
-        uint4* o = reinterpret_cast<uint4*>(a.xp + p * a.D + col);
-        o[0] = x[0];
-        if (!half) o[1] = x[1];
+        uint16_t* o = a.xp + p * a.D + col;
+        store_stream16(o, x[0]);
+        if (!half) store_stream16(o + 8, x[1]);
     }
     if (a.q) {
         uint8_t* o = a.q + p * a.D + col;
         if (a.wide) {
-            *reinterpret_cast<uint4*>(o) = q;
+            store_stream16(o, q);
         } else {
-            reinterpret_cast<uint2*>(o)[0] = make_uint2(q.x, q.y);
-            if (!half) reinterpret_cast<uint2*>(o)[1] = make_uint2(q.z, q.w);
+            store_stream(o, make_uint2(q.x, q.y));
+            if (!half) store_stream(o + 8, make_uint2(q.z, q.w));
         }
         if ((threadIdx.x & 7) == 0) a.scales[p * ((a.D + 127) / 128) + col / 128] = scale;
     }
@@ -195,8 +213,8 @@ __device__ __forceinline__ void put_token(const DispatchArgs& a, int64_t t, cons
             const int64_t col = (int64_t)(u + i * ustep) * kUnit + lane * 16;
             const uint16_t* src = a.x + t * a.D + col;
             x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-            if (u + i * ustep < units && col < a.D) x[i][0] = load_stream(src);
-            if (u + i * ustep < units && col + 8 < a.D) x[i][1] = load_stream(src + 8);
+            if (u + i * ustep < units && col < a.D) x[i][0] = *reinterpret_cast<const uint4*>(src);
+            if (u + i * ustep < units && col + 8 < a.D) x[i][1] = *reinterpret_cast<const uint4*>(src + 8);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -278,7 +296,10 @@ __global__ __launch_bounds__(kDispatchThreads) void dispatch_fused_kernel(Dispat
 }
 
 // Copy and cast by a known order: workgroups below `tokens` take one token each,
-// the others 64 rows each and zero those without a slot.
+// the others kZeroRows rows each and zero those without a slot (few rows a
+// workgroup, since the rows past the last group come together).
+constexpr int kZeroRows = 16;
+
 template <int U>
 __global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs a, int tokens) {
     __shared__ int s_row[kWave];
@@ -293,11 +314,10 @@ __global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs
         __syncthreads();
         put_token<U>(a, t, s_row, wave, kDispatchWaves, units);
     } else {
-        const int64_t lo = (t - tokens) * kWave, p = lo + lane;
-        const int slot = p < a.P ? a.slots[p] : 0;
-        int turn = 0;
-        for (uint64_t left = __ballot(slot < 0); left; left &= left - 1, ++turn)
-            if (turn % kDispatchWaves == wave) zero_row(a, lo + __builtin_ctzll(left), 0, 1, units);
+        const int64_t lo = (t - tokens) * kZeroRows + wave * (kZeroRows / kDispatchWaves), p = lo + lane;
+        const int slot = lane < kZeroRows / kDispatchWaves && p < a.P ? a.slots[p] : 0;
+        for (uint64_t left = __ballot(slot < 0); left; left &= left - 1)
+            zero_row(a, lo + __builtin_ctzll(left), 0, 1, units);
     }
 }
 
@@ -333,11 +353,10 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(
     const int64_t t = blockIdx.x;
     if (t >= T) {
         if (blockIdx.y > 0) return;
-        const int64_t n = T * k, lo = (t - T) * kWave, p = lo + lane;
-        const int slot = p < P ? slots[p] : 0;
-        int turn = 0;
-        for (uint64_t left = __ballot(p < P && (slot < 0 || slot >= n)); left; left &= left - 1, ++turn) {
-            if (turn % 4 != wave) continue;
+        const int64_t n = T * k, lo = (t - T) * kZeroRows + wave * (kZeroRows / 4), p = lo + lane;
+        const bool mine = lane < kZeroRows / 4 && p < P;
+        const int slot = mine ? slots[p] : 0;
+        for (uint64_t left = __ballot(mine && (slot < 0 || slot >= n)); left; left &= left - 1) {
             uint16_t* row = dyp + (lo + __builtin_ctzll(left)) * D;
             for (int64_t col = lane * 8; col < D; col += 512)
                 *reinterpret_cast<uint4*>(row + col) = make_uint4(0, 0, 0, 0);
@@ -392,11 +411,14 @@ hipError_t launch_dispatch(const DispatchArgs& args, int cus, hipStream_t stream
         if (e != hipSuccess) return e;
     }
     const int waves = a.E > 512 ? 8 : 16;        // their counts take at most 32 KiB of LDS
-    const size_t shmem = (3 * (size_t)a.E + 1 + (size_t)waves * a.E) * sizeof(int);
-    hipLaunchKernelGGL(rank_kernel, dim3((unsigned)runs), dim3(waves * kWave), shmem, stream, a, run);
+    const size_t shmem = (2 * (size_t)a.E + 1 + (size_t)waves * a.E) * sizeof(int);
+    if (waves == 8)
+        hipLaunchKernelGGL(rank_kernel<8>, dim3((unsigned)runs), dim3(512), shmem, stream, a, run);
+    else
+        hipLaunchKernelGGL(rank_kernel<16>, dim3((unsigned)runs), dim3(1024), shmem, stream, a, run);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !moves) return e;
-    const int64_t blocks = a.T + (a.P + kWave - 1) / kWave;
+    const int64_t blocks = a.T + (a.P + kZeroRows - 1) / kZeroRows;
     if (units > kDispatchWaves)
         hipLaunchKernelGGL(dispatch_kernel<2>, dim3((unsigned)blocks), dim3(kDispatchThreads), 0, stream, a, (int)a.T);
     else
@@ -415,7 +437,7 @@ hipError_t launch_combine(const uint16_t* yp, int64_t P, int64_t D, const int32_
 hipError_t launch_combine_grad(const uint16_t* dy, const uint16_t* yp, int64_t P, int64_t D,
                                const int32_t* rows, const int32_t* slots, int64_t T, int k,
                                const float* weights, uint16_t* dyp, float* dw, int cus, hipStream_t stream) {
-    const int64_t blocks = T + (P + 63) / 64;
+    const int64_t blocks = T + (P + kZeroRows - 1) / kZeroRows;
     // few tokens: a workgroup for each slot instead of each token
     const int64_t split = T < 4 * (int64_t)cus ? k : 1;
     hipLaunchKernelGGL(combine_grad_kernel, dim3((unsigned)blocks, (unsigned)split), dim3(256), 0, stream, dy, yp, P, D, rows, slots,

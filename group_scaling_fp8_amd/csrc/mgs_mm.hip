@@ -445,9 +445,15 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     start_loads(t, t, 1, 1);
     wait_some_or_none<LOADS>(1);
     __syncthreads();
-    v8i fa = fragment(s_a[0] + a_at, lo, hi), fb[NT];
+    // fa holds the bytes of A's first row of fragments, ob B's fragments; where
+    // registers allow it (kAhead), oa holds that row already as bf16 and fa the
+    // second row's bytes.
+    constexpr bool kAhead = !FAST && MT <= 4;
+    v8i fa = fragment(s_a[0] + a_at + (kAhead ? 16 * kBK : 0), lo, hi);
+    Op oa, ob[NT];
+    if constexpr (kAhead) oa = Op(fragment(s_a[0] + a_at, lo, hi));
 #pragma unroll
-    for (int j = 0; j < NT; ++j) fb[j] = fragment(s_b[0] + b_at + b_row(j) * kBK, lo, hi);
+    for (int j = 0; j < NT; ++j) ob[j] = Op(fragment(s_b[0] + b_at + b_row(j) * kBK, lo, hi));
 
     int third = 0;           // of s_scale: tiles walked modulo 3
     int drain = 0;           // whether a tile's stores (and nothing else) follow the loads of this tile's second step
@@ -492,11 +498,9 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             sb_inv = 1.0f / sb_next;
             sb_next = col_scale(t, next, k + 1);
         }
-        Op ob[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) ob[j] = Op(fb[j]);
-        auto multiply = [&](int i, const v8i& v) {
-            const Op a(v);
+        // Row i of fragments. Between the instructions stand the additions of the
+        // row before it and, exact, the conversions of the row after it.
+        auto multiply = [&](int i, const Op& a) {
             if constexpr (WGRAD) {
                 Op::mfma(ob, a, acc[i]);
             } else {
@@ -506,41 +510,68 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
                 for (int j = 0; j < NT; ++j) now[j] = v4f{0, 0, 0, 0};
                 Op::mfma(ob, a, now);
                 promote((i + MT - 1) % MT);
-                // an instruction, then the additions of a sum that an earlier
-                // one finished
-#pragma unroll
-                for (int j = 0; j < NT * (FAST ? 1 : 4); ++j) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x002, FAST ? 5 : 3, 0);
-                }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) part[j] = now[j];
                 part_scale = f;
             }
+            if constexpr (!WGRAD || !FAST) {
+#pragma unroll
+                for (int j = 0; j < NT * (FAST ? 1 : 4); ++j) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, FAST ? 5 : WGRAD ? 1 : 2, 0);
+                }
+            }
         };
-        v8i ahead = {}, last = {};
+        auto next_step = [&] {
+            // the next step's bytes are in LDS
+            wait_some_or_none<STORES + (WGRAD ? 1 : 0)>(k == 0 ? drain : 0);
+            __syncthreads();
+            if constexpr (!WGRAD) {
+                scale[((ring + k + 2) & 3) * BM + srow] = 1.0f / s_raw[(ring + k) & 1][threadIdx.x];
+                start_scales(t, next, k + 3);
+            }
+            start_loads(t, next, k + 2, cur);
+        };
+        if constexpr (!kAhead) {
+            v8i ahead = {}, last = {};
 #pragma unroll
-        for (int i = 0; i < MT - 2; ++i) {
-            ahead = fragment(ta + (i + 1) * 16 * kBK, lo, hi);
-            if (i == MT - 3) last = fragment(ta + (MT - 1) * 16 * kBK, lo, hi);
-            multiply(i, fa);
-            fa = ahead;
+            for (int i = 0; i < MT - 2; ++i) {
+                ahead = fragment(ta + (i + 1) * 16 * kBK, lo, hi);
+                if (i == MT - 3) last = fragment(ta + (MT - 1) * 16 * kBK, lo, hi);
+                multiply(i, Op(fa));
+                fa = ahead;
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            next_step();
+            multiply(MT - 2, Op(fa));
             __builtin_amdgcn_sched_barrier(0);
-        }
-        // the next step's bytes are in LDS
-        wait_some_or_none<STORES + (WGRAD ? 1 : 0)>(k == 0 ? drain : 0);
-        __syncthreads();
-        if constexpr (!WGRAD) {
-            scale[((ring + k + 2) & 3) * BM + srow] = 1.0f / s_raw[(ring + k) & 1][threadIdx.x];
-            start_scales(t, next, k + 3);
-        }
-        start_loads(t, next, k + 2, cur);
-        multiply(MT - 2, fa);
-        __builtin_amdgcn_sched_barrier(0);
-        fa = fragment(na, lo, hi);
-        multiply(MT - 1, last);
+            fa = fragment(na, lo, hi);
+            multiply(MT - 1, Op(last));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) fb[j] = fragment(nb + b_row(j) * kBK, lo, hi);
+            for (int j = 0; j < NT; ++j) ob[j] = Op(fragment(nb + b_row(j) * kBK, lo, hi));
+        } else {
+            // fa: bytes of the row after oa's
+            v8i fb[NT];
+#pragma unroll
+            for (int i = 0; i < MT - 1; ++i) {
+                const v8i ahead = i < MT - 2 ? fragment(ta + (i + 2) * 16 * kBK, lo, hi) : fragment(na, lo, hi);
+                const Op after(fa);
+                multiply(i, oa);
+                oa = after;
+                fa = ahead;
+                __builtin_amdgcn_sched_barrier(0);
+                if (i == MT - 3) next_step();
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) fb[j] = fragment(nb + b_row(j) * kBK, lo, hi);
+            const v8i ahead = fragment(na + 16 * kBK, lo, hi);
+            const Op after(fa);
+            multiply(MT - 1, oa);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) ob[j] = Op(fb[j]);
+            oa = after;
+            fa = ahead;
+        }
         __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!WGRAD) promote(MT - 1);

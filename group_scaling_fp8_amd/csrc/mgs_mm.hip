@@ -286,30 +286,38 @@ __device__ __forceinline__ void wait_some_or_none(int some) {
 
 // One workgroup a CU walks tiles b, b + grid, ...: the first loads of a tile are
 // issued before the stores of the one before it, which then drain under the
-// tile's first steps.
-template <int BM, int BN, int WM, int WN, bool WGRAD, bool FAST, bool F32>
-__global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs p) {
-    constexpr int WAVES = BM / WM * (BN / WN);
+// tile's first steps. With PARTS > 1 a workgroup has one tile, whose steps are
+// dealt out to as many sets of waves, each with buffers of its own; their sums
+// are added in LDS at the end.
+template <int BM, int BN, int WM, int WN, int PARTS, bool WGRAD, bool FAST, bool F32>
+__global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel(MmArgs p) {
+    constexpr int WAVES = BM / WM * (BN / WN);             // of one part
     constexpr int MT = WM / 16, NT = WN / 16;
     constexpr int LOADS = (BM + BN) / 8 / WAVES;           // a wave's loads a step
     constexpr int STORES = MT * NT / (F32 ? 1 : 2);        // a wave's stores of a whole tile
     static_assert(WN <= 128 && 128 % WN == 0, "a wave's columns share one scale block");
-    __shared__ __align__(128) uint8_t s_a[2][BM * kBK];
-    __shared__ __align__(128) uint8_t s_b[2][BN * kBK];
+    __shared__ __align__(128) uint8_t s_all_a[PARTS][2][BM * kBK];
+    __shared__ __align__(128) uint8_t s_all_b[PARTS][2][BN * kBK];
     // block128: a ring of four steps' reciprocal scales of the rows; wgrad: the
     // scales of the last, this and the next tile's rows and columns
-    __shared__ __align__(16) float s_scale[WGRAD ? 3 * WAVES * 64 : 4 * BM];
-    __shared__ float s_raw[2][WGRAD ? 1 : WAVES * 64];     // block128: the scale each thread fetches, of two steps
+    __shared__ __align__(16) float s_all_scale[PARTS][WGRAD ? 3 * WAVES * 64 : 4 * BM];
+    __shared__ float s_all_raw[PARTS][2][WGRAD ? 1 : WAVES * 64];     // block128: the scale each thread fetches, of two steps
     __shared__ Groups s_groups;
     const int lane = threadIdx.x & (kWave - 1);
-    const int wave = uniform((int)(threadIdx.x / kWave));
+    const int part_of = PARTS > 1 ? uniform((int)(threadIdx.x / (WAVES * kWave))) : 0;
+    const int tid = (int)threadIdx.x - part_of * (WAVES * kWave);
+    const int wave = uniform(tid / kWave);
+    uint8_t(*const s_a)[BM * kBK] = s_all_a[part_of];
+    uint8_t(*const s_b)[BN * kBK] = s_all_b[part_of];
+    float* const s_scale = s_all_scale[part_of];
+    float(*const s_raw)[WGRAD ? 1 : WAVES * 64] = s_all_raw[part_of];
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
     const int64_t nkb = (p.K + kBK - 1) / kBK, nnb = (p.N + 127) / 128;
 
     // ---- the tiles ----
     const int row_tiles = (int)((p.N + BM - 1) / BM);                            // wgrad: down one matrix
     const int col_tiles = (int)(((WGRAD ? p.K : p.N) + BN - 1) / BN);
-    if (wave == 0) s_groups.fill(p.offsets, p.G, (int)p.M, WGRAD ? 16 : 1, BM);
+    if (threadIdx.x < kWave) s_groups.fill(p.offsets, p.G, (int)p.M, WGRAD ? 16 : 1, BM);
     __syncthreads();
     auto end_of = [&](int g) { return g < 0 ? 0 : uniform(s_groups.end[g]); };
     int total;       // tiles; the host has checked that 32 bits hold them
@@ -357,7 +365,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             t.sa = p.a_scales + t.m0 * nkb;
             t.sb = p.b_scales + (e * nnb + min((int64_t)(t.n0 + wn) / 128, nnb - 1)) * nkb;
         }
-        t.steps = max((t.len + kBK - 1) / kBK, kMinSteps<WGRAD>);
+        t.steps = max((t.len + kBK * PARTS - 1) / (kBK * PARTS), kMinSteps<WGRAD>);
         return t;
     };
     int b = blockIdx.x;
@@ -375,7 +383,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     // step k of t, which is past its end where it is one of the next tile
     auto start_loads = [&](const Tile& t, const Tile& next, int k, int buf) {
         const bool over = k >= t.steps;
-        const int kk = (over ? k - t.steps : k) * kBK, len = over ? next.len : t.len, skip = over ? next.skip : t.skip;
+        const int kk = ((over ? k - t.steps : k) * PARTS + part_of) * kBK, len = over ? next.len : t.len, skip = over ? next.skip : t.skip;
         const v4i a{over ? next.a[0] : t.a[0], over ? next.a[1] : t.a[1], over ? next.a[2] : t.a[2], t.a[3]};
         const v4i b{over ? next.b[0] : t.b[0], over ? next.b[1] : t.b[1], over ? next.b[2] : t.b[2], t.b[3]};
         load_tile<WAVES, BM>(a, va, stride, chunk_a, kk, len, skip, lds_a + buf * (BM * kBK), wave);
@@ -389,7 +397,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     // would also be a wait for the stores before it.
     int ring = 0;            // steps of the tiles before this one
     const int nkb32 = (int)nkb;
-    const int srow = WGRAD ? (int)threadIdx.x % (BM + BN) : (int)threadIdx.x % BM;
+    const int srow = WGRAD ? tid % (BM + BN) : tid % BM;
     const uint32_t lds_raw = uniform((int)lds_address(s_raw)) + wave * 256;
     const uint32_t lds_scale = uniform((int)lds_address(s_scale)) + wave * 256;
     const float *p_sa = p.a_scales, *p_sb = p.b_scales;
@@ -399,11 +407,11 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     };
     auto row_scales = [&](const Tile& t, const Tile& next, int k) {
         const bool over = k >= t.steps;
-        return (over ? next.sa : t.sa) + min(over ? k - t.steps : k, nkb32 - 1);
+        return (over ? next.sa : t.sa) + min((over ? k - t.steps : k) * PARTS + part_of, nkb32 - 1);
     };
     auto col_scale = [&](const Tile& t, const Tile& next, int k) {
         const bool over = k >= t.steps;
-        return scalar_load((over ? next.sb : t.sb) + min(over ? k - t.steps : k, nkb32 - 1));
+        return scalar_load((over ? next.sb : t.sb) + min((over ? k - t.steps : k) * PARTS + part_of, nkb32 - 1));
     };
     auto start_scales = [&](const Tile& t, const Tile& next, int k) {
         const float* s = row_scales(t, next, k);
@@ -438,7 +446,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
     } else {
         s_scale[srow] = 1.0f / row_scales(t, t, 0)[row_offset(t, t, 0)];
         s_scale[BM + srow] = 1.0f / row_scales(t, t, 1)[row_offset(t, t, 0)];
-        s_raw[0][threadIdx.x] = row_scales(t, t, 2)[row_offset(t, t, 0)];
+        s_raw[0][tid] = row_scales(t, t, 2)[row_offset(t, t, 0)];
     }
     float sb_next = WGRAD ? 1.0f : col_scale(t, t, 0);
     start_loads(t, t, 0, 0);
@@ -527,7 +535,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
             wait_some_or_none<STORES + (WGRAD ? 1 : 0)>(k == 0 ? drain : 0);
             __syncthreads();
             if constexpr (!WGRAD) {
-                scale[((ring + k + 2) & 3) * BM + srow] = 1.0f / s_raw[(ring + k) & 1][threadIdx.x];
+                scale[((ring + k + 2) & 3) * BM + srow] = 1.0f / s_raw[(ring + k) & 1][tid];
                 start_scales(t, next, k + 3);
             }
             start_loads(t, next, k + 2, cur);
@@ -575,6 +583,24 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64, 2) void mm_kernel(MmArgs 
         __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!WGRAD) promote(MT - 1);
+    if constexpr (PARTS > 1) {
+        static_assert(PARTS == 2 && sizeof(s_all_b) >= sizeof(acc) * WAVES * 64, "the second part's sums");
+        v4f* const sums = reinterpret_cast<v4f*>(s_all_b) + tid;
+        load_wait();         // no load into the buffers is left, the last ones past the tile's end among them
+        __syncthreads();
+        if (part_of == 1) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sums[(i * NT + j) * (WAVES * 64)] = acc[i][j];
+        }
+        __syncthreads();
+        if (part_of == 1) return;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] += sums[(i * NT + j) * (WAVES * 64)];
+    }
     if (t.len == 0) {        // whatever the scales of no rows are
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -820,20 +846,20 @@ hipError_t launch_few(const MmArgs& p, bool f32, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, bool WGRAD, bool FAST>
+template <int BM, int BN, int WM, int WN, int PARTS, bool WGRAD, bool FAST>
 hipError_t launch(const MmArgs& p, bool f32, int cus, hipStream_t stream) {
-    constexpr int threads = BM / WM * (BN / WN) * 64;
+    constexpr int threads = BM / WM * (BN / WN) * 64 * PARTS;
     constexpr int per_cu = 512 / threads;        // workgroups of at most 256 registers a lane
     // block128: every group, and the rows past the last one, may end inside a tile
     const int64_t down = WGRAD ? p.G * ((p.N + BM - 1) / BM) : p.M / BM + (p.offsets ? p.G + 1 : 1);
     const int64_t tiles = down * ((p.cols + BN - 1) / BN);
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    const int64_t blocks = tiles < cus * per_cu ? tiles : cus * per_cu;
+    const int64_t blocks = PARTS > 1 || tiles < cus * per_cu ? tiles : cus * per_cu;
     if (f32)
-        hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, WGRAD, FAST, true>), dim3((unsigned)blocks), dim3(threads), 0,
+        hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, PARTS, WGRAD, FAST, true>), dim3((unsigned)blocks), dim3(threads), 0,
                            stream, p);
     else
-        hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, WGRAD, FAST, false>), dim3((unsigned)blocks), dim3(threads), 0,
+        hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, PARTS, WGRAD, FAST, false>), dim3((unsigned)blocks), dim3(threads), 0,
                            stream, p);
     return hipGetLastError();
 }
@@ -852,15 +878,18 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   2048 x 4096 x 4096, half the CUs: 66 and 48) and, for wgrad, where the contraction is long or the tiles are many
 //   (16640 x 8192 x 5120 in 16 groups: 839 and 948; 4096 x 2048 x 2048 in 8
 //   groups, four steps a tile: 40 and 32).
-// - 128 x 128 tiles otherwise, two workgroups a CU; block128 with binary32 sums
-//   has no registers for more (256 x 128: 1591 and 1491).
+// - 128 x 128 tiles otherwise, two workgroups a CU (block128 with binary32 sums
+//   has no registers for more: 256 x 128 took 1591, 128 x 128 1491); where they
+//   leave half the CUs idle, two sets of waves share a tile's contraction (256 x
+//   4096 x 4096: 32 to 27; wgrad 8192 x 1024 x 1024: 44 to 37; with binary32 sums
+//   block128 does not gain).
 template <bool WGRAD, bool FAST>
 hipError_t launch_sized(const MmArgs& p, bool f32, int cus, hipStream_t stream) {
     const int64_t groups = p.offsets ? p.G : 1;
     if constexpr (WGRAD) {
         const int64_t tiles = groups * up(p.N, 256) * up(p.K, 256);
         if (tiles >= cus && (p.M / groups >= 2048 || tiles >= 4 * cus))
-            return launch<256, 256, 128, 64, true, FAST>(p, f32, cus, stream);
+            return launch<256, 256, 128, 64, 1, true, FAST>(p, f32, cus, stream);
     } else {
         const int64_t rows = up(p.M, groups);
         if (rows <= 20) return launch_few<16>(p, f32, stream);
@@ -868,10 +897,14 @@ hipError_t launch_sized(const MmArgs& p, bool f32, int cus, hipStream_t stream) 
         if (groups == 1 && up(p.M, 64) * up(p.N, kFewCols) <= cus) return launch_few<64>(p, f32, stream);
         if constexpr (FAST) {
             if ((up(p.M, 256) + groups / 2) * up(p.N, 256) >= (groups == 1 ? cus : 2 * cus))
-                return launch<256, 256, 128, 64, false, true>(p, f32, cus, stream);
+                return launch<256, 256, 128, 64, 1, false, true>(p, f32, cus, stream);
         }
     }
-    return launch<128, 128, 64, 64, WGRAD, FAST>(p, f32, cus, stream);
+    if constexpr (WGRAD || FAST) {
+        const int64_t tiles = (WGRAD ? groups * up(p.N, 128) : p.M / 128 + (p.offsets ? p.G + 1 : 1)) * up(p.cols, 128);
+        if (2 * tiles <= cus) return launch<128, 128, 64, 64, 2, WGRAD, FAST>(p, f32, cus, stream);
+    }
+    return launch<128, 128, 64, 64, 1, WGRAD, FAST>(p, f32, cus, stream);
 }
 
 }  // namespace

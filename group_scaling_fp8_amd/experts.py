@@ -63,6 +63,18 @@ def mgs_moe_rows(T: int, top_k: int, n_experts: int, align: int = 16) -> int:
     return _order_sizes(int(T), int(top_k), int(n_experts), int(align))[0]
 
 
+def _workspace(need: int, device, stream) -> torch.Tensor:
+    """Workspace of one call, freed when the call returns: from the memory of
+    the stream that the call runs on, so that only later work on that stream
+    can be given it while the kernels still run."""
+    if stream is None:
+        return torch.empty((need,), dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty((need,), dtype=torch.uint8, device=device)
+
+
 def _dispatch(x, ids, n_experts, align, pow2, cast, permuted, stream):
     _need(ids, "expert_ids", (torch.int32,), 2)
     T, k = ids.shape
@@ -86,7 +98,7 @@ def _dispatch(x, ids, n_experts, align, pow2, cast, permuted, stream):
     if permuted:
         xp = torch.empty((P, D), dtype=torch.bfloat16, device=dev)
     if need:
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+        ws = _workspace(need, dev, stream)
     moves = P > 0 and D > 0
     st = lib().mgs_moe_dispatch(_ptr(x) if moves else None, T, D, ids.data_ptr(), k, E, align,
                                 MGS_FLAG_POW2_SCALE if pow2 else 0, P, offsets.data_ptr(), rows.data_ptr(),
@@ -216,7 +228,8 @@ def mgs_mm_block128(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_
     kind = _out_type(out_dtype)
     y = _out(y, (M, N), out_dtype, a.device, "y")
     st = lib().mgs_mm_block128(a.data_ptr(), a_scales.data_ptr(), M, K, b.data_ptr(), b_scales.data_ptr(), E, N,
-                               _ptr(offsets), MGS_FLAG_FAST_ACCUM if fast_accum else 0, kind, y.data_ptr(), _stream_handle(stream, a))
+                               _ptr(offsets), MGS_FLAG_FAST_ACCUM if fast_accum else 0, kind, y.data_ptr(),
+                               _stream_handle(stream, a))
     check("mgs_mm_block128", st)
     return y
 

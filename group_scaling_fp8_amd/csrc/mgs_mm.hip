@@ -284,11 +284,26 @@ __device__ __forceinline__ void wait_some_or_none(int some) {
 #endif
 }
 
-// One workgroup a CU walks tiles b, b + grid, ...: the first loads of a tile are
-// issued before the stores of the one before it, which then drain under the
-// tile's first steps. With PARTS > 1 a workgroup has one tile, whose steps are
-// dealt out to as many sets of waves, each with buffers of its own; their sums
-// are added in LDS at the end.
+// As many workgroups as the CUs hold at a time (one of 256 x 256 tiles, two of
+// 128 x 128) walk tiles b, b + grid, ...: the first loads of a tile are issued
+// before the stores of the one before it, which then drain under the tile's
+// first steps. With PARTS > 1 a workgroup has one tile, whose steps are dealt
+// out to as many sets of waves, each with buffers of its own; their sums are
+// added in LDS at the end.
+//
+// What bounds it, by form (rates of dense products, MI355X; the library's plain
+// E4M3 product reaches 2600 TFLOP/s at 8192^3, its bf16 product 1400):
+//   256 x 256 fast    block128 2150 TFLOP/s, wgrad 2780 (16384 x 8192 x 8192). A
+//                     step's 32 matrix instructions a wave, two waves a SIMD,
+//                     take 2048 cycles; block128 adds 128 fmas a wave for the
+//                     scaled sums, which stand in the gaps between them, and the
+//                     eight waves read 192 KiB of LDS in about 1500 cycles beside
+//                     the 512 that the loads write.
+//   exact             block128 1080 TFLOP/s, wgrad 1580: the bf16 instructions
+//                     take twice the cycles, and every wave widens the bytes of
+//                     its fragments itself, which takes issue slots.
+//   few tiles         latency: two steps' loads (64 KiB a CU) are in flight, and a
+//                     CU takes in 35 to 45 KB/us whatever the form.
 template <int BM, int BN, int WM, int WN, int PARTS, bool WGRAD, bool FAST, bool F32>
 __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel(MmArgs p) {
     constexpr int WAVES = BM / WM * (BN / WN);             // of one part

@@ -253,3 +253,25 @@ def test_past_two_to_the_31_elements():
     assert torch.equal(back, x)
     dyp, dw = mgs.mgs_moe_combine_grad(x, xp, rows, slots, torch.ones((T, k), device="cuda"))
     assert torch.equal(dyp[last], xp[last]) and torch.equal(dyp[262150], xp[262150])
+
+
+def test_more_workgroups_than_one_grid_dimension_holds():
+    """17 million tokens of eight columns: a workgroup each passes 2^32 threads."""
+    T, E, D = 17_000_000, 4, 8
+    t = torch.arange(T, device="cuda")
+    ids = (t % E).to(torch.int32)[:, None].contiguous()
+    x = (t[:, None] % 251 - 125).to(torch.bfloat16).expand(T, D).contiguous()
+    off, rows, slots, q, s, xp = mgs.mgs_moe_dispatch(x, ids, E, permuted=True)
+    per = T // E
+    full = (per + 15) // 16 * 16
+    assert off.tolist() == [full * (e + 1) for e in range(E)]
+    assert torch.equal(rows[:, 0].long(), t % E * full + t // E)
+    assert torch.equal(xp[rows[:, 0].long()], x)
+    assert torch.equal(slots[rows[:, 0].long()].long(), t)
+    pads = slots < 0
+    assert int(pads.sum()) == slots.shape[0] - T and not bool(xp[pads].any())
+    w = torch.full((T, 1), 2.0, device="cuda")
+    assert torch.equal(mgs.mgs_moe_combine(xp, rows, w), 2 * x)
+    dyp, dw = mgs.mgs_moe_combine_grad(x, xp, rows, slots, w)
+    assert torch.equal(dyp[rows[:, 0].long()], 2 * x) and not bool(dyp[pads].any())
+    assert torch.equal(dw[:, 0], (t % 251 - 125).float() ** 2 * D)

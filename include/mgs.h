@@ -323,7 +323,9 @@ int mgs_copy(const void *src, void *dst, int64_t bytes, void *stream);
  * A slot i = t * top_k + s is the s-th expert choice of token t. An id outside
  * [0, n_experts) drops its slot. Row counts are not known on the host, so row
  * arrays have n_rows rows, at least mgs_moe_rows; the rows that no slot takes
- * (the ends of the groups and the rows past the last one) are zero.
+ * (the ends of the groups and the rows past the last one) are zero. Rows past
+ * the last end offset belong to no group: mgs_quant_groups_dim0_t, whose
+ * outputs mgs_mm_wgrad reads, leaves their columns of q_t as they are.
  */
 #define MGS_MOE_MAX_TOP_K 64
 #define MGS_FLAG_ACCUMULATE 4u /* mgs_mm_wgrad: add to dw (fp32 only) */
@@ -354,6 +356,7 @@ int mgs_moe_workspace_bytes(int64_t T, int32_t top_k, int32_t n_experts, int64_t
  *   x           (T, D) bf16 (may be NULL when xp and q are).
  *   expert_ids  (T, top_k) int32.
  *   flags       0 or MGS_FLAG_POW2_SCALE.
+ *   n_rows      at least what mgs_moe_rows gives.
  *   offsets     (n_experts) int32 end offsets, written: group e holds expert
  *               e's slots in slot order, filled up to a multiple of align.
  *   rows        (T, top_k) int32, written: the row of each slot, -1 if dropped.

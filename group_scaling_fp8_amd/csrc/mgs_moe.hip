@@ -19,11 +19,10 @@ namespace {
 // ---- the order ---------------------------------------------------------------
 //
 // Up to kMoeFusedSlots slots, every workgroup of the one dispatch kernel counts
-// all of them for itself (1 token, 8 of 64 experts, 5120 columns: 5.2 us; 24 in
-// launches of their own for counts, ranks and copies). More are ranked first by
-// rank_kernel, one workgroup of 16 waves for each run of slots (with more than
-// one run, hist_kernel counts each run's slots before it), and dispatch reads
-// rows and slots (6702 slots: 10 us; 66560: 6 and 13).
+// all of them for itself (1 token, 8 of 64 experts, 5120 columns: 5.2 us; 1117
+// tokens, 6 of 61, 4112 columns: 12.7). More are ranked first, by one workgroup
+// of 16 waves for each run of slots: hist_kernel counts, rank_kernel writes rows
+// and slots, and dispatch_kernel reads them (66560 slots: 6 and 13 us).
 
 // The lanes (of those with `held`) whose expert is this lane's: one ballot for
 // each bit of the id.
@@ -119,12 +118,10 @@ __global__ __launch_bounds__(WAVES * 64) void rank_kernel(DispatchArgs a, int64_
         int count[WAVES], sum = 0, prior = 0;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) count[w] = s_wave[w * E + e];
-        if (gridDim.x > 1) {
-            for (int r = 0; r < (int)gridDim.x; ++r) {
-                const int c = a.hist[(int64_t)r * E + e];
-                if (r < (int)blockIdx.x) prior += c;
-                sum += c;
-            }
+        for (int r = 0; r < (int)gridDim.x; ++r) {
+            const int c = a.hist[(int64_t)r * E + e];
+            if (r < (int)blockIdx.x) prior += c;
+            sum += c;
         }
         int before = prior;
 #pragma unroll
@@ -132,7 +129,7 @@ __global__ __launch_bounds__(WAVES * 64) void rank_kernel(DispatchArgs a, int64_
             s_wave[w * E + e] = before;
             before += count[w];
         }
-        s_total[e] = gridDim.x > 1 ? sum : before;
+        s_total[e] = sum;
     }
     __syncthreads();
     if (wave == 0) group_starts(s_total, s_start, E, a.align);
@@ -206,80 +203,107 @@ __device__ __forceinline__ void zero_row(const DispatchArgs& a, int64_t p, int u
     }
 }
 
-// Units u0, u0 + ustep, ... of token t, cast once and written to the rows of its
-// k slots; U units' loads are under way at a time.
-template <int U>
-__device__ __forceinline__ void put_token(const DispatchArgs& a, int64_t t, const int* rows, int u0, int ustep, int units) {
-    const int lane = threadIdx.x & (kWave - 1);
-    for (int u = u0; u < units; u += U * ustep) {
-        uint4 x[U][2];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int64_t col = (int64_t)(u + i * ustep) * kUnit + lane * 16;
-            const uint16_t* src = a.x + t * a.D + col;
-            x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-            if (u + i * ustep < units && col < a.D) x[i][0] = *reinterpret_cast<const uint4*>(src);
-            if (u + i * ustep < units && col + 8 < a.D) x[i][1] = *reinterpret_cast<const uint4*>(src + 8);
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int64_t col = (int64_t)(u + i * ustep) * kUnit + lane * 16;
-            const float s = group_scale(row8_max(mag_fold(mag_max8(mag_max8(0u, x[i][0]), x[i][1]))), a.pow2 != 0);
-            const uint2 lo = cast8_group(x[i][0], s), hi = cast8_group(x[i][1], s);
-            if (u + i * ustep < units && col < a.D)
-                for (int j = 0; j < a.k; ++j)
-                    if (rows[j] >= 0) put(a, rows[j], col, col + 8 >= a.D, x[i], make_uint4(lo.x, lo.y, hi.x, hi.y), s);
-        }
-    }
+// Unit u of token t: 16 columns a lane, zeros past the end.
+__device__ __forceinline__ void load_piece(const DispatchArgs& a, int64_t t, int u, uint4 (&x)[2]) {
+    const int64_t col = (int64_t)u * kUnit + (threadIdx.x & (kWave - 1)) * 16;
+    const uint16_t* src = a.x + t * a.D + col;
+    x[0] = x[1] = make_uint4(0, 0, 0, 0);
+    if (col < a.D) x[0] = *reinterpret_cast<const uint4*>(src);
+    if (col + 8 < a.D) x[1] = *reinterpret_cast<const uint4*>(src + 8);
 }
 
-// Everything in one launch, for few slots: workgroups below `tokens` take one
-// token each, all take a share of the rows without a slot, and grid.y splits the
-// columns. Every workgroup finds the order by itself.
-__global__ __launch_bounds__(kDispatchThreads) void dispatch_fused_kernel(DispatchArgs a, int tokens) {
+// Its cast, made once, to the rows of the token's k slots.
+__device__ __forceinline__ void put_piece(const DispatchArgs& a, const int* rows, int u, const uint4 (&x)[2]) {
+    const int64_t col = (int64_t)u * kUnit + (threadIdx.x & (kWave - 1)) * 16;
+    const float s = group_scale(row8_max(mag_fold(mag_max8(mag_max8(0u, x[0]), x[1]))), a.pow2 != 0);
+    const uint2 lo = cast8_group(x[0], s), hi = cast8_group(x[1], s);
+    if (col >= a.D) return;
+    for (int j = 0; j < a.k; ++j)
+        if (rows[j] >= 0) put(a, rows[j], col, col + 8 >= a.D, x, make_uint4(lo.x, lo.y, hi.x, hi.y), s);
+}
+
+// Everything in one launch, for few slots: workgroups below `groups` take `per`
+// consecutive tokens each, all take a share of the rows without a slot, and
+// grid.y splits the columns. Every workgroup finds the order by itself, while
+// its first loads of x are on their way.
+constexpr int kFusedThreads = 512;
+constexpr int kFusedWaves = kFusedThreads / kWave;
+
+__global__ __launch_bounds__(kFusedThreads) void dispatch_fused_kernel(DispatchArgs a, int groups, int per) {
     extern __shared__ int smem[];
     const int E = a.E, k = a.k, tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    int* s_total = smem;                // (E) slots of each expert
-    int* s_before = s_total + E;        // (E) those before this workgroup's token
-    int* s_start = s_before + E;        // (E + 1) first row of each group
-    int* s_row = s_start + E + 1;       // (k) rows of this workgroup's token
-    const int64_t t = blockIdx.x, n = a.T * k, first = min(t * k, n);
-    for (int e = tid; e < E; e += kDispatchThreads) s_total[e] = s_before[e] = 0;
-    __syncthreads();
-    for (int64_t i = tid; i < n; i += kDispatchThreads) {
-        const int e = a.ids[i];
-        if (e >= 0 && e < E) {
-            atomicAdd(&s_total[e], 1);
-            if (i < first) atomicAdd(&s_before[e], 1);
-        }
+    int* s_before = smem;               // (E) slots of each expert before this workgroup's tokens
+    int* s_total = s_before + E;        // (E) all the others, then all
+    int* s_start = s_total + E;         // (E + 1) first row of each group
+    int* s_row = s_start + E + 1;       // (per, k) rows of this workgroup's tokens
+    const int n = (int)(a.T * k), t0 = blockIdx.x * per;
+    const int tokens = (int)blockIdx.x < groups ? min(per, (int)a.T - t0) : 0;
+    const int first = tokens ? t0 * k : n, last = first + tokens * k;
+    const int units = (int)((a.D + kUnit - 1) / kUnit), u0 = blockIdx.y, mine = (units - u0 + (int)gridDim.y - 1) / (int)gridDim.y;
+    // a wave's pieces: (token, unit) pairs of this workgroup, one in kFusedWaves
+    const int pieces = tokens * mine;
+    auto unit_of = [&](int i) { return u0 + i % mine * (int)gridDim.y; };
+    uint4 x[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = wave + j * kFusedWaves;
+        if (i < pieces) load_piece(a, t0 + i / mine, unit_of(i), x[j]);
     }
+    for (int e = tid; e < 2 * E; e += kFusedThreads) s_before[e] = 0;
+    __syncthreads();
+    for (int base = tid; base < n; base += 8 * kFusedThreads) {
+        int e[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) e[c] = base + c * kFusedThreads < n ? a.ids[base + c * kFusedThreads] : -1;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (e[c] >= 0 && e[c] < E) atomicAdd(&smem[base + c * kFusedThreads < first ? e[c] : E + e[c]], 1);
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += kFusedThreads) s_total[e] += s_before[e];
     __syncthreads();
     if (wave == 0) {
         group_starts(s_total, s_start, E, a.align);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-        if (t < tokens) {               // k is at most one wave's lanes
-            const int e = lane < k ? a.ids[first + lane] : -1;
+        for (int base = first; base < last; base += kWave) {
+            const int i = base + lane, e = i < last ? a.ids[i] : -1;
             const bool held = e >= 0 && e < E;
             const uint64_t same = same_expert(e, held, E);
+            const int below = __popcll(same & lanes_below());
             int row = -1;
-            if (held) row = s_start[e] + s_before[e] + __popcll(same & lanes_below());
+            if (held) row = s_start[e] + s_before[e] + below;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (held && below == 0) s_before[e] += __popcll(same);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             if (row >= a.P) row = -1;
-            if (lane < k) {
-                s_row[lane] = row;
-                if (blockIdx.y == 0) {
-                    a.rows[first + lane] = row;
-                    if (row >= 0) a.slots[row] = (int)(first + lane);
+            if (i < last) {
+                s_row[i - first] = row;
+                if (u0 == 0) {
+                    a.rows[i] = row;
+                    if (row >= 0) a.slots[row] = i;
                 }
             }
         }
     }
     __syncthreads();
-    const int units = (int)((a.D + kUnit - 1) / kUnit), u0 = blockIdx.y;
     if (blockIdx.x == 0 && u0 == 0)
-        for (int e = tid; e < E; e += kDispatchThreads) a.offsets[e] = s_start[e + 1];
+        for (int e = tid; e < E; e += kFusedThreads) a.offsets[e] = s_start[e + 1];
+
+    for (int i = wave; i < pieces; i += 2 * kFusedWaves) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int at = i + j * kFusedWaves;
+            if (at < pieces) put_piece(a, s_row + at / mine * k, unit_of(at), x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int at = i + (j + 2) * kFusedWaves;
+            if (at < pieces) load_piece(a, t0 + at / mine, unit_of(at), x[j]);
+        }
+    }
 
     // rows without a slot: place r of every group, dealt out over all waves
-    const int waves = gridDim.x * kDispatchWaves, w = blockIdx.x * kDispatchWaves + wave;
+    const int waves = gridDim.x * kFusedWaves, w = blockIdx.x * kFusedWaves + wave;
     const int places = E * a.align, tail = (int)(a.P - s_start[E]);
     for (int base = w; base < places + tail; base += waves * kWave) {
         const int i = base + lane * waves;
@@ -297,7 +321,6 @@ __global__ __launch_bounds__(kDispatchThreads) void dispatch_fused_kernel(Dispat
             zero_row(a, row, u0, gridDim.y, units);
         }
     }
-    if (t < tokens) put_token<1>(a, t, s_row, u0 + wave * gridDim.y, kDispatchWaves * gridDim.y, units);
 }
 
 // Copy and cast by a known order: workgroups below `tokens` take one token each,
@@ -328,7 +351,15 @@ __global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs
             s_row[threadIdx.x] = p;
         }
         __syncthreads();
-        put_token<U>(a, t, s_row, wave, kDispatchWaves, units);
+        for (int u = wave; u < units; u += U * kDispatchWaves) {
+            uint4 x[U][2];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (u + i * kDispatchWaves < units) load_piece(a, t, u + i * kDispatchWaves, x[i]);
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (u + i * kDispatchWaves < units) put_piece(a, s_row, u + i * kDispatchWaves, x[i]);
+        }
     } else {
         const int64_t lo = (t - tokens) * kZeroRows + wave * (kZeroRows / kDispatchWaves), p = lo + lane;
         const int slot = lane < kZeroRows / kDispatchWaves && p < a.P ? a.slots[p] : 0;
@@ -411,31 +442,32 @@ hipError_t launch_dispatch(const DispatchArgs& args, int cus, hipStream_t stream
     const int64_t n = a.T * a.k, units = (a.D + kUnit - 1) / kUnit;
     const bool moves = a.xp || a.q;
     if (n <= kMoeFusedSlots) {
-        // enough workgroups that a wave has about one row to zero
-        const int64_t spare = (a.P - n + kDispatchWaves - 1) / kDispatchWaves;
+        // two workgroups a CU, and at least so many that a wave has about one row
+        // to zero
+        const int64_t per = a.T > 2 * cus ? (a.T + 2 * cus - 1) / (2 * cus) : 1, groups = (a.T + per - 1) / per;
+        const int64_t spare = (a.P - n + kFusedWaves - 1) / kFusedWaves;
         int64_t blocks = spare < cus ? spare : cus;
-        blocks = blocks > a.T ? blocks : a.T;
-        const size_t shmem = (3 * (size_t)a.E + 1 + kWave) * sizeof(int);
-        int64_t split = cus / (blocks > 0 ? blocks : 1);
-        split = split < 1 ? 1 : split > units ? (units > 0 ? units : 1) : split;
-        hipLaunchKernelGGL(dispatch_fused_kernel, dim3((unsigned)(blocks > 0 ? blocks : 1), (unsigned)split),
-                           dim3(kDispatchThreads), shmem, stream, a, (int)a.T);
+        blocks = blocks > groups ? blocks : groups;
+        blocks = blocks > 1 ? blocks : 1;
+        const size_t shmem = (3 * (size_t)a.E + 1 + (size_t)(per * a.k)) * sizeof(int);
+        int64_t split = cus / blocks;
+        split = split > units ? units : split;
+        hipLaunchKernelGGL(dispatch_fused_kernel, dim3((unsigned)blocks, (unsigned)(split > 1 ? split : 1)),
+                           dim3(kFusedThreads), shmem, stream, a, (int)groups, (int)per);
         return hipGetLastError();
     }
     const int64_t runs = moe_runs(n), run = moe_run(n);
-    if (runs > 1) {
-        hipLaunchKernelGGL(hist_kernel, dim3((unsigned)runs), dim3(1024), a.E * sizeof(int), stream, a.ids, n, run,
-                           a.E, a.hist);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
+    hipLaunchKernelGGL(hist_kernel, dim3((unsigned)runs), dim3(1024), a.E * sizeof(int), stream, a.ids, n, run, a.E,
+                       a.hist);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     const int waves = a.E > 512 ? 8 : 16;        // their counts take at most 32 KiB of LDS
     const size_t shmem = (2 * (size_t)a.E + 1 + (size_t)waves * a.E) * sizeof(int);
     if (waves == 8)
         hipLaunchKernelGGL(rank_kernel<8>, dim3((unsigned)runs), dim3(512), shmem, stream, a, run);
     else
         hipLaunchKernelGGL(rank_kernel<16>, dim3((unsigned)runs), dim3(1024), shmem, stream, a, run);
-    const hipError_t e = hipGetLastError();
+    e = hipGetLastError();
     if (e != hipSuccess || !moves) return e;
     const int64_t blocks = a.T + (a.P + kZeroRows - 1) / kZeroRows;
     if (units > kDispatchWaves)

@@ -346,7 +346,7 @@ enum { MGS_OUT_BF16 = 0, MGS_OUT_F32 = 1 };
  */
 int mgs_moe_rows(int64_t T, int32_t top_k, int32_t n_experts, int32_t align, int64_t *n_rows);
 
-/* Bytes of workspace that mgs_moe_dispatch needs: 0 up to 8192 slots, else at
+/* Bytes of workspace that mgs_moe_dispatch needs: 0 up to 32768 slots, else at
  * most 256 * n_experts. Its contents need no preparation and do not matter
  * afterwards. Host only. */
 int mgs_moe_workspace_bytes(int64_t T, int32_t top_k, int32_t n_experts, int64_t *bytes);

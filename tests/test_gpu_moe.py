@@ -275,3 +275,19 @@ def test_more_workgroups_than_one_grid_dimension_holds():
     dyp, dw = mgs.mgs_moe_combine_grad(x, xp, rows, slots, w)
     assert torch.equal(dyp[rows[:, 0].long()], 2 * x) and not bool(dyp[pads].any())
     assert torch.equal(dw[:, 0], (t % 251 - 125).float() ** 2 * D)
+
+
+@pytest.mark.parametrize("T,k,E,align,kind", [
+    (32768, 1, 5, 16, "mixed"), (4681, 7, 300, 32, "mixed"), (32769, 1, 1024, 16, "skewed"), (16400, 2, 513, 16, "mixed"),
+    (9000, 4, 512, 16, "one"), (300001, 2, 3, 16, "mixed"), (10900, 3, 7, 4096, "mixed"), (513, 1, 2, 16, "dropped")])
+def test_order_around_the_limit_of_one_launch(T, k, E, align, kind):
+    """32768 slots are the last that one launch takes; runs past 524288 slots are
+    ranked in several parts a wave."""
+    test_order(T, k, E, align, kind)
+
+
+@pytest.mark.parametrize("T,k,E,D,kind,pow2", [
+    (520, 64, 70, 4104, "mixed", False), (33001, 1, 9, 72, "skewed", True), (4096, 8, 33, 1040, "mixed", False),
+    (3000, 1, 40, 2072, "dropped", False)])
+def test_dispatch_around_the_limit_of_one_launch(T, k, E, D, kind, pow2):
+    test_dispatch(T, k, E, D, kind, pow2)

@@ -60,7 +60,7 @@ struct Tile {
     int m0, n0;              // block128: first row and column; wgrad: first n and k
     int row_end;             // rows past it are not stored
     int g;
-    const float *sa, *sb;    // block128: scales of the first row and of the wave's columns
+    const float* scales;     // block128: of the first row, or of the columns, as the wave fetches
 };
 
 // Loads run two steps ahead of the sums, and block128's scales three, at most
@@ -126,22 +126,28 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // modulo 8, or for B's rows of a bf16 output, which lanes read in runs of four
 // out of eight, the row's bits 0, 1 and 3.
 
-// Starts the load of one step's rows of 128 bytes into LDS, 16 bytes a lane
-// straight from memory. Rows past the valid ones repeat the last one (their
-// products are never stored); bytes outside the contraction are zero.
-template <int WAVES, int ROWS>
-__device__ __forceinline__ void load_tile(v4i src, uint32_t voff, uint32_t stride, int chunk, int kk, int len, int skip,
-                                          uint32_t lds, int wave) {
+// A wave's share of the loads of one step's rows of 128 bytes into LDS, 16 bytes
+// a lane straight from memory. Rows past the valid ones repeat the last one
+// (their products are never stored); bytes outside the contraction are zero.
+struct Loads {
+    v4i src;
+    uint32_t voff, step, lds;        // of the lane's first row, to the next load's, of the wave's first line
+    bool inside;
+
+    __device__ __forceinline__ Loads(v4i src, uint32_t voff, uint32_t step, int chunk, int kk, int len, int skip, uint32_t lds)
+        : src(src), step(step), lds(lds) {
 #ifdef __HIP_DEVICE_COMPILE__
-    asm volatile("" : "+s"(kk));        // offsets are made here, not kept in registers for each kk
+        asm volatile("" : "+s"(kk));        // offsets are made here, not kept in registers for each kk
 #endif
-    const int at = kk + chunk * 16;
-    const bool inside = at < len && at >= skip;
-#pragma unroll
-    for (int j = 0; j < ROWS / 8 / WAVES; ++j)
-        load16_lds(src, inside ? voff + (j * WAVES * 8 * stride + (uint32_t)kk) : kOutOfRange,
-                   lds + (j * WAVES + wave) * 1024);
-}
+        const int at = kk + chunk * 16;
+        inside = at < len && at >= skip;
+        this->voff = voff + (uint32_t)kk;
+    }
+    template <int WAVES>
+    __device__ __forceinline__ void start(int j) const {
+        load16_lds(src, inside ? voff + j * step : kOutOfRange, lds + j * WAVES * 1024);
+    }
+};
 
 // A lane's two chunks of the line at p.
 __device__ __forceinline__ v8i fragment(const uint8_t* p, int lo, int hi) {
@@ -175,8 +181,10 @@ struct Operand<true> {
     template <int N>
     __device__ __forceinline__ static void mfma(const Operand (&a)[N], const Operand& b, v4f (&c)[N]) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            c[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j].v, b.v, c[j], 0, 0, 0, 0, 0, 0);
+        for (int j = 0; j < N; ++j) mfma(a[j], b, c[j]);
+    }
+    __device__ __forceinline__ static void mfma(const Operand& a, const Operand& b, v4f& c) {
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, c, 0, 0, 0, 0, 0, 0);
     }
 };
 
@@ -202,13 +210,6 @@ struct Operand<false> {
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
-}
-
-// One value for all lanes through the scalar cache, so that waiting for it does
-// not wait for vector loads.
-__device__ __forceinline__ float scalar_load(const float* p) {
-    const uint64_t at = (uint64_t)uniform((int64_t)reinterpret_cast<uint64_t>(p));
-    return *reinterpret_cast<const __attribute__((address_space(4))) float*>(at);
 }
 
 // The groups as the casts read their ends (a running maximum, clamped to [0, M],
@@ -313,9 +314,10 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     static_assert(WN <= 128 && 128 % WN == 0, "a wave's columns share one scale block");
     __shared__ __align__(128) uint8_t s_all_a[PARTS][2][BM * kBK];
     __shared__ __align__(128) uint8_t s_all_b[PARTS][2][BN * kBK];
-    // block128: a ring of four steps' reciprocal scales of the rows; wgrad: the
-    // scales of the last, this and the next tile's rows and columns
-    __shared__ __align__(16) float s_all_scale[PARTS][WGRAD ? 3 * WAVES * 64 : 4 * BM];
+    // block128: a ring of four steps' reciprocal scales of the rows (the first BM
+    // of each) and columns; wgrad: the scales of the last, this and the next
+    // tile's rows and columns
+    __shared__ __align__(16) float s_all_scale[PARTS][(WGRAD ? 3 : 4) * WAVES * 64];
     __shared__ float s_all_raw[PARTS][2][WGRAD ? 1 : WAVES * 64];     // block128: the scale each thread fetches, of two steps
     __shared__ Groups s_groups;
     const int lane = threadIdx.x & (kWave - 1);
@@ -328,6 +330,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     float(*const s_raw)[WGRAD ? 1 : WAVES * 64] = s_all_raw[part_of];
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
     const int64_t nkb = (p.K + kBK - 1) / kBK, nnb = (p.N + 127) / 128;
+    const bool down = wave * 64 < BM;        // this wave fetches scales of rows, else of columns
 
     // ---- the tiles ----
     const int row_tiles = (int)((p.N + BM - 1) / BM);                            // wgrad: down one matrix
@@ -361,7 +364,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
             t.row_end = (int)p.N;
             t.a = descriptor(p.a, t.m0 * p.M + from, p.N * p.M);
             t.b = descriptor(p.b, t.n0 * p.M + from, p.K * p.M);
-            t.sa = t.sb = nullptr;
+            t.scales = nullptr;
         } else {
             // tiles are numbered by group, then in patches
             t.g = uniform(s_groups.find(uniform(L / col_tiles), p.G));
@@ -377,8 +380,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
             const int64_t e = max(t.g, 0);
             t.a = descriptor(p.a, t.m0 * p.K, p.M * p.K);
             t.b = descriptor(p.b, (e * p.N + t.n0) * p.K, p.G * p.N * p.K);
-            t.sa = p.a_scales + t.m0 * nkb;
-            t.sb = p.b_scales + (e * nnb + min((int64_t)(t.n0 + wn) / 128, nnb - 1)) * nkb;
+            const int64_t block = min((int64_t)t.n0 / 128 + (wave - BM / 64) % (BN / 128), nnb - 1);
+            t.scales = down ? p.a_scales + t.m0 * nkb : p.b_scales + (e * nnb + block) * nkb;
         }
         t.steps = max((t.len + kBK * PARTS - 1) / (kBK * PARTS), kMinSteps<WGRAD>);
         return t;
@@ -396,46 +399,53 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     const uint32_t va = (wave * 8 + lrow) * stride + chunk_a * 16, vb = (wave * 8 + lrow) * stride + chunk_b * 16;
     const uint32_t lds_a = uniform((int)lds_address(s_a)), lds_b = uniform((int)lds_address(s_b));
     // step k of t, which is past its end where it is one of the next tile
-    auto start_loads = [&](const Tile& t, const Tile& next, int k, int buf) {
+    auto loads_a = [&](const Tile& t, const Tile& next, int k, int buf) {
         const bool over = k >= t.steps;
-        const int kk = ((over ? k - t.steps : k) * PARTS + part_of) * kBK, len = over ? next.len : t.len, skip = over ? next.skip : t.skip;
         const v4i a{over ? next.a[0] : t.a[0], over ? next.a[1] : t.a[1], over ? next.a[2] : t.a[2], t.a[3]};
-        const v4i b{over ? next.b[0] : t.b[0], over ? next.b[1] : t.b[1], over ? next.b[2] : t.b[2], t.b[3]};
-        load_tile<WAVES, BM>(a, va, stride, chunk_a, kk, len, skip, lds_a + buf * (BM * kBK), wave);
-        load_tile<WAVES, BN>(b, vb, stride, chunk_b, kk, len, skip, lds_b + buf * (BN * kBK), wave);
+        return Loads(a, va, WAVES * 8 * stride, chunk_a, ((over ? k - t.steps : k) * PARTS + part_of) * kBK,
+                     over ? next.len : t.len, over ? next.skip : t.skip, lds_a + buf * (BM * kBK) + wave * 1024);
     };
-    // block128: a thread fetches one row's scale, three steps ahead, and puts its
-    // reciprocal into a ring of four steps when it has come; the columns' scale
-    // comes one step ahead through the scalar cache. wgrad: a thread fetches one
-    // scale of the next tile's rows and columns. Like the tiles, the scales come
-    // by loads that the compiler does not wait for: a wait for one of them alone
-    // would also be a wait for the stores before it.
+    auto loads_b = [&](const Tile& t, const Tile& next, int k, int buf) {
+        const bool over = k >= t.steps;
+        const v4i b{over ? next.b[0] : t.b[0], over ? next.b[1] : t.b[1], over ? next.b[2] : t.b[2], t.b[3]};
+        return Loads(b, vb, WAVES * 8 * stride, chunk_b, ((over ? k - t.steps : k) * PARTS + part_of) * kBK,
+                     over ? next.len : t.len, over ? next.skip : t.skip, lds_b + buf * (BN * kBK) + wave * 1024);
+    };
+    auto start_loads = [&](const Tile& t, const Tile& next, int k, int buf) {
+        const Loads a = loads_a(t, next, k, buf), b = loads_b(t, next, k, buf);
+#pragma unroll
+        for (int j = 0; j < BM / 8 / WAVES; ++j) a.template start<WAVES>(j);
+#pragma unroll
+        for (int j = 0; j < BN / 8 / WAVES; ++j) b.template start<WAVES>(j);
+    };
+    // block128: a thread fetches one scale, three steps ahead: the first BM of a
+    // row, the waves behind them of a block of columns, one for all lanes. One
+    // step ahead, when it has come, it puts the reciprocal into a ring of four
+    // steps. wgrad: a thread fetches one scale of the next tile's rows and columns.
+    // Like the tiles, the scales come by loads that the compiler does not wait for:
+    // a wait for one of them alone would also be a wait for the stores before it.
     int ring = 0;            // steps of the tiles before this one
     const int nkb32 = (int)nkb;
     const int srow = WGRAD ? tid % (BM + BN) : tid % BM;
     const uint32_t lds_raw = uniform((int)lds_address(s_raw)) + wave * 256;
     const uint32_t lds_scale = uniform((int)lds_address(s_scale)) + wave * 256;
     const float *p_sa = p.a_scales, *p_sb = p.b_scales;
-    auto row_offset = [&](const Tile& t, const Tile& next, int k) {
+    const uint32_t scale_pitch = down ? (uint32_t)nkb : 0;
+    auto scale_offset = [&](const Tile& t, const Tile& next, int k) {
         const int rows = (int)p.M - 1 - (k >= t.steps ? next.m0 : t.m0);
-        return (uint32_t)min(srow, rows) * (uint32_t)nkb32;
+        return (uint32_t)min(srow, rows) * scale_pitch;
     };
-    auto row_scales = [&](const Tile& t, const Tile& next, int k) {
+    auto scales = [&](const Tile& t, const Tile& next, int k) {
         const bool over = k >= t.steps;
-        return (over ? next.sa : t.sa) + min((over ? k - t.steps : k) * PARTS + part_of, nkb32 - 1);
-    };
-    auto col_scale = [&](const Tile& t, const Tile& next, int k) {
-        const bool over = k >= t.steps;
-        return scalar_load((over ? next.sb : t.sb) + min((over ? k - t.steps : k) * PARTS + part_of, nkb32 - 1));
+        return (over ? next.scales : t.scales) + min((over ? k - t.steps : k) * PARTS + part_of, nkb32 - 1);
     };
     auto start_scales = [&](const Tile& t, const Tile& next, int k) {
-        const float* s = row_scales(t, next, k);
-        load4_lds(descriptor(reinterpret_cast<const uint8_t*>(s), 0, 0x7FFFFFFF), row_offset(t, next, k) * 4,
+        const float* s = scales(t, next, k);
+        load4_lds(descriptor(reinterpret_cast<const uint8_t*>(s), 0, 0x7FFFFFFF), scale_offset(t, next, k) * 4,
                   lds_raw + ((ring + k) & 1) * (WAVES * 256));
     };
     auto start_tile_scales = [&](const Tile& t, int third) {
         static_assert(!WGRAD || BM + BN <= WAVES * 64, "a thread fetches one scale");
-        const bool down = wave * 64 < BM;        // a wave's are all rows or all columns
         const int64_t first = down ? t.m0 : t.n0;
         const int at = min(down ? srow : srow - BM, (int)min((down ? p.N : p.K) - 1 - first, (int64_t)BM + BN));
         const float* s = (down ? p_sa : p_sb) + first * p.G + t.g;
@@ -459,11 +469,10 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     if constexpr (WGRAD) {
         start_tile_scales(t, 0);
     } else {
-        s_scale[srow] = 1.0f / row_scales(t, t, 0)[row_offset(t, t, 0)];
-        s_scale[BM + srow] = 1.0f / row_scales(t, t, 1)[row_offset(t, t, 0)];
-        s_raw[0][tid] = row_scales(t, t, 2)[row_offset(t, t, 0)];
+        s_scale[tid] = 1.0f / scales(t, t, 0)[scale_offset(t, t, 0)];
+        s_raw[1][tid] = scales(t, t, 1)[scale_offset(t, t, 0)];
+        s_raw[0][tid] = scales(t, t, 2)[scale_offset(t, t, 0)];
     }
-    float sb_next = WGRAD ? 1.0f : col_scale(t, t, 0);
     start_loads(t, t, 0, 0);
     start_loads(t, t, 1, 1);
     wait_some_or_none<LOADS>(1);
@@ -499,11 +508,9 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     float part_scale = 0.0f;
 #pragma unroll
     for (int j = 0; j < NT; ++j) part[j] = v4f{0, 0, 0, 0};
-    auto promote = [&](int i) {
+    auto promote = [&](int i, int j) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(part[j][c], part_scale, acc[i][j][c]);
+        for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(part[j][c], part_scale, acc[i][j][c]);
     };
     // One step: the rows of fragments of A in turn, each read while the one
     // before it is multiplied. The barrier stands before the last two rows,
@@ -516,27 +523,33 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     for (int k = 0; k < steps; ++k) {
         const int cur = (ring + k) & 1;
         const uint8_t *ta = s_a[cur] + a_at, *na = s_a[cur ^ 1] + a_at, *nb = s_b[cur ^ 1] + b_at;
-        float sb_inv = 0.0f;
+        float sb_inv = 0.0f, raw = 0.0f;
         if constexpr (!WGRAD) {
-            sb_inv = 1.0f / sb_next;
-            sb_next = col_scale(t, next, k + 1);
+            sb_inv = scale[((ring + k) & 3) * (WAVES * 64) + BM + wn / 128 * 64];
+            raw = s_raw[(ring + k + 1) & 1][tid];
         }
+        auto publish = [&] {
+            if constexpr (!WGRAD) scale[((ring + k + 1) & 3) * (WAVES * 64) + tid] = 1.0f / raw;
+        };
         // Row i of fragments. Between the instructions stand the additions of the
         // row before it and, exact, the conversions of the row after it.
         auto multiply = [&](int i, const Op& a) {
             if constexpr (WGRAD) {
                 Op::mfma(ob, a, acc[i]);
             } else {
-                const float f = scale[((ring + k) & 3) * BM + wm + i * 16 + fr] * sb_inv;
+                const float f = scale[((ring + k) & 3) * (WAVES * 64) + wm + i * 16 + fr] * sb_inv;
                 v4f now[NT];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) now[j] = v4f{0, 0, 0, 0};
                 Op::mfma(ob, a, now);
-                promote((i + MT - 1) % MT);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) promote((i + MT - 1) % MT, j);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) part[j] = now[j];
                 part_scale = f;
             }
+            // reads first: what they bring is waited for in the next row
+            if constexpr (FAST) __builtin_amdgcn_sched_group_barrier(0x100, WGRAD ? 2 : 3, 0);
             if constexpr (!WGRAD || !FAST) {
 #pragma unroll
                 for (int j = 0; j < NT * (FAST ? 1 : 4); ++j) {
@@ -545,15 +558,37 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
                 }
             }
         };
+        // Fast: the same with then(j) after each instruction.
+        auto multiply_and = [&](int i, const Op& a, auto&& then) {
+            float f = 0.0f;
+            v4f now[NT];
+            if constexpr (!WGRAD) f = scale[((ring + k) & 3) * (WAVES * 64) + wm + i * 16 + fr] * sb_inv;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if constexpr (WGRAD && FAST) {
+                    Op::mfma(ob[j], a, acc[i][j]);
+                } else if constexpr (FAST) {
+                    now[j] = v4f{0, 0, 0, 0};
+                    Op::mfma(ob[j], a, now[j]);
+                    promote((i + MT - 1) % MT, j);
+                }
+                then(j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (!WGRAD) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) part[j] = now[j];
+                part_scale = f;
+            }
+        };
         auto next_step = [&] {
             // the next step's bytes are in LDS
             wait_some_or_none<STORES + (WGRAD ? 1 : 0)>(k == 0 ? drain : 0);
             __syncthreads();
             if constexpr (!WGRAD) {
-                scale[((ring + k + 2) & 3) * BM + srow] = 1.0f / s_raw[(ring + k) & 1][tid];
                 start_scales(t, next, k + 3);
             }
-            start_loads(t, next, k + 2, cur);
+            if constexpr (!FAST) start_loads(t, next, k + 2, cur);
         };
         if constexpr (!kAhead) {
             v8i ahead = {}, last = {};
@@ -561,17 +596,32 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
             for (int i = 0; i < MT - 2; ++i) {
                 ahead = fragment(ta + (i + 1) * 16 * kBK, lo, hi);
                 if (i == MT - 3) last = fragment(ta + (MT - 1) * 16 * kBK, lo, hi);
+                if (i == 1) publish();
                 multiply(i, Op(fa));
                 fa = ahead;
                 __builtin_amdgcn_sched_barrier(0);
             }
             next_step();
-            multiply(MT - 2, Op(fa));
-            __builtin_amdgcn_sched_barrier(0);
-            fa = fragment(na, lo, hi);
-            multiply(MT - 1, Op(last));
+            if constexpr (FAST) {
+                // a load, or in the last row a load and the next step's fragment of
+                // B, after each instruction: eight in a row would hold the wave up
+                static_assert(NT == BM / 8 / WAVES && NT == BN / 8 / WAVES, "as many loads as instructions a row");
+                const Loads a = loads_a(t, next, k + 2, cur);
+                multiply_and(MT - 2, Op(fa), [&](int j) { a.template start<WAVES>(j); });
+                fa = fragment(na, lo, hi);
+                const Loads b = loads_b(t, next, k + 2, cur);
+                multiply_and(MT - 1, Op(last), [&](int j) {
+                    b.template start<WAVES>(j);
+                    ob[j] = Op(fragment(nb + b_row(j) * kBK, lo, hi));
+                });
+            } else {
+                multiply(MT - 2, Op(fa));
+                __builtin_amdgcn_sched_barrier(0);
+                fa = fragment(na, lo, hi);
+                multiply(MT - 1, Op(last));
 #pragma unroll
-            for (int j = 0; j < NT; ++j) ob[j] = Op(fragment(nb + b_row(j) * kBK, lo, hi));
+                for (int j = 0; j < NT; ++j) ob[j] = Op(fragment(nb + b_row(j) * kBK, lo, hi));
+            }
         } else {
             // fa: bytes of the row after oa's
             v8i fb[NT];
@@ -579,6 +629,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
             for (int i = 0; i < MT - 1; ++i) {
                 const v8i ahead = i < MT - 2 ? fragment(ta + (i + 2) * 16 * kBK, lo, hi) : fragment(na, lo, hi);
                 const Op after(fa);
+                if (i == 1) publish();
                 multiply(i, oa);
                 oa = after;
                 fa = ahead;
@@ -597,7 +648,10 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
         }
         __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (!WGRAD) promote(MT - 1);
+    if constexpr (!WGRAD) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) promote(MT - 1, j);
+    }
     if constexpr (PARTS > 1) {
         static_assert(PARTS == 2 && sizeof(s_all_b) >= sizeof(acc) * WAVES * 64, "the second part's sums");
         v4f* const sums = reinterpret_cast<v4f*>(s_all_b) + tid;

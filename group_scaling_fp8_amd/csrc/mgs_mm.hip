@@ -477,11 +477,13 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     start_loads(t, t, 1, 1);
     wait_some_or_none<LOADS>(1);
     __syncthreads();
-    // fa holds the bytes of A's first row of fragments, ob B's fragments; where
-    // registers allow it (kAhead), oa holds that row already as bf16 and fa the
-    // second row's bytes.
+    // fa and fa1 hold the bytes of A's first two rows of fragments, ob B's
+    // fragments; where registers allow it (kAhead), oa holds the first row already
+    // as bf16 and fa the second row's bytes.
     constexpr bool kAhead = !FAST && MT <= 4;
     v8i fa = fragment(s_a[0] + a_at + (kAhead ? 16 * kBK : 0), lo, hi);
+    v8i fa1 = {};
+    if constexpr (!kAhead) fa1 = fragment(s_a[0] + a_at + 16 * kBK, lo, hi);
     Op oa, ob[NT];
     if constexpr (kAhead) oa = Op(fragment(s_a[0] + a_at, lo, hi));
 #pragma unroll
@@ -512,8 +514,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(part[j][c], part_scale, acc[i][j][c]);
     };
-    // One step: the rows of fragments of A in turn, each read while the one
-    // before it is multiplied. The barrier stands before the last two rows,
+    // One step: the rows of fragments of A in turn, each read while the two
+    // before it are multiplied. The barrier stands before the last two rows,
     // whose fragments are already in registers: behind it the other buffer is
     // complete and this one free, so the loads of the step after next and the
     // first fragments of the next step are on their way during the rest; at a
@@ -591,14 +593,13 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
             if constexpr (!FAST) start_loads(t, next, k + 2, cur);
         };
         if constexpr (!kAhead) {
-            v8i ahead = {}, last = {};
 #pragma unroll
             for (int i = 0; i < MT - 2; ++i) {
-                ahead = fragment(ta + (i + 1) * 16 * kBK, lo, hi);
-                if (i == MT - 3) last = fragment(ta + (MT - 1) * 16 * kBK, lo, hi);
+                const v8i ahead = fragment(ta + (i + 2) * 16 * kBK, lo, hi);
                 if (i == 1) publish();
                 multiply(i, Op(fa));
-                fa = ahead;
+                fa = fa1;
+                fa1 = ahead;
                 __builtin_amdgcn_sched_barrier(0);
             }
             next_step();
@@ -610,17 +611,19 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
                 multiply_and(MT - 2, Op(fa), [&](int j) { a.template start<WAVES>(j); });
                 fa = fragment(na, lo, hi);
                 const Loads b = loads_b(t, next, k + 2, cur);
-                multiply_and(MT - 1, Op(last), [&](int j) {
+                multiply_and(MT - 1, Op(fa1), [&](int j) {
                     b.template start<WAVES>(j);
                     ob[j] = Op(fragment(nb + b_row(j) * kBK, lo, hi));
                 });
+                fa1 = fragment(na + 16 * kBK, lo, hi);
             } else {
                 multiply(MT - 2, Op(fa));
                 __builtin_amdgcn_sched_barrier(0);
                 fa = fragment(na, lo, hi);
-                multiply(MT - 1, Op(last));
+                multiply(MT - 1, Op(fa1));
 #pragma unroll
                 for (int j = 0; j < NT; ++j) ob[j] = Op(fragment(nb + b_row(j) * kBK, lo, hi));
+                fa1 = fragment(na + 16 * kBK, lo, hi);
             }
         } else {
             // fa: bytes of the row after oa's

@@ -4,7 +4,8 @@
 // q = E4M3(fl32(x * s)), over blocks that the block-128 product reads:
 // 1 x 128 for activations and gradients, 128 x 128 for weights. One pass: a
 // block's values stay in registers between its maximum and its cast, so both
-// kernels are bound by memory traffic. Times are of single launches on MI355X.
+// kernels are bound by memory traffic. Times are of launches back to back on
+// MI355X.
 #include "mgs_block128_device.hpp"
 #include "mgs_experts.hpp"
 
@@ -13,7 +14,7 @@ namespace mgs {
 namespace {
 
 // A wave casts 512 columns of one row: 16 lanes hold one block of 128. 16640 x
-// 8192, 0.41 GB: 70 us, 5.9 TB/s.
+// 8192, 0.41 GB: 70 us, 5.9 TB/s (streaming stores: 74).
 __global__ __launch_bounds__(256) void rows128_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                       int units, int pow2, uint8_t* __restrict__ q,
                                                       float* __restrict__ scales) {
@@ -32,25 +33,28 @@ __global__ __launch_bounds__(256) void rows128_kernel(const uint16_t* __restrict
 }
 
 // One block of 128 x 128 a workgroup: thread t holds 8 columns (t & 15) of the
-// rows t / 16 + 16 j. The transposed order goes through LDS: both orders cost one
-// read of w. 16 x 8192 x 5120, 2.68 GB with both orders: 500 us, 5.4 TB/s.
+// rows 4 (t / 16) + j and 64 + 4 (t / 16) + j, j < 4, so that loads and stores of a
+// row are whole lines. The transposed order goes through LDS, four rows of a
+// column at a time: both orders cost one read of w. Streaming stores: the
+// outputs are larger than the caches. 16 x 8192 x 5120, 2.68 GB with both orders:
+// 530 us back to back, 5.1 TB/s (plain stores of q: 557).
 __global__ __launch_bounds__(256) void blocks128_kernel(const uint16_t* __restrict__ w, int64_t N, int64_t K,
                                                         int pow2, uint8_t* __restrict__ q, float* __restrict__ scales,
                                                         uint8_t* __restrict__ q_t, float* __restrict__ scales_t) {
     __shared__ uint32_t s_max[4];
-    __shared__ uint8_t s_t[128][128 + 4];
+    __shared__ uint32_t s_t[128][32 + 1];
     const int64_t nbk = (K + 127) / 128, nbn = (N + 127) / 128;
     const int64_t bk = blockIdx.x % nbk, rest = blockIdx.x / nbk, bn = rest % nbn, e = rest / nbn;
-    const int cv = threadIdx.x & 15, r0 = threadIdx.x / 16;
+    const int cv = threadIdx.x & 15, rq = threadIdx.x / 16;
     const int64_t col = bk * 128 + cv * 8, row0 = bn * 128;
+    auto row_of = [&](int j) { return row0 + rq * 4 + (j & 3) + (j >> 2) * 64; };
     const uint16_t* we = w + e * N * K;
     uint4 v[8];
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int64_t r = row0 + r0 + 16 * j;
         v[j] = make_uint4(0, 0, 0, 0);
-        if (r < N && col < K) v[j] = load_stream(we + r * K + col);
+        if (row_of(j) < N && col < K) v[j] = load_stream(we + row_of(j) * K + col);
         m = mag_max8(m, v[j]);
     }
     m = mag_fold(m);
@@ -64,25 +68,31 @@ __global__ __launch_bounds__(256) void blocks128_kernel(const uint16_t* __restri
         scales[(e * nbn + bn) * nbk + bk] = s;
         if (scales_t) scales_t[(e * nbk + bk) * nbn + bn] = s;
     }
+    uint2 c[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int r = r0 + 16 * j;
-        const uint2 c = cast8_group(v[j], s);
-        if (row0 + r < N && col < K) *reinterpret_cast<uint2*>(q + (e * N + row0 + r) * K + col) = c;
-        if (q_t) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s_t[cv * 8 + i][r] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
-        }
+        c[j] = cast8_group(v[j], s);
+        if (row_of(j) < N && col < K) store_stream(q + (e * N + row_of(j)) * K + col, c[j]);
     }
     if (!q_t) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t lo[4], hi[4];
+        transpose4x4(c[4 * h].x, c[4 * h + 1].x, c[4 * h + 2].x, c[4 * h + 3].x, lo);
+        transpose4x4(c[4 * h].y, c[4 * h + 1].y, c[4 * h + 2].y, c[4 * h + 3].y, hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s_t[cv * 8 + i][h * 16 + rq] = lo[i];
+            s_t[cv * 8 + 4 + i][h * 16 + rq] = hi[i];
+        }
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 128 * 16; i += 256) {
-        const int c = i / 16, r = (i & 15) * 8;
-        if (bk * 128 + c >= K || row0 + r >= N) continue;
-        uint2 o;
-        o.x = *reinterpret_cast<const uint32_t*>(&s_t[c][r]);
-        o.y = *reinterpret_cast<const uint32_t*>(&s_t[c][r + 4]);
-        *reinterpret_cast<uint2*>(q_t + (e * K + bk * 128 + c) * N + row0 + r) = o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int i = j * 256 + threadIdx.x, k = i / 8, r = (i & 7) * 16;
+        if (bk * 128 + k >= K || row0 + r >= N) continue;
+        const uint32_t* t = &s_t[k][r / 4];
+        store_stream16(q_t + (e * K + bk * 128 + k) * N + row0 + r, make_uint4(t[0], t[1], t[2], t[3]));
     }
 }
 

@@ -757,10 +757,14 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
 // wave order.
 constexpr int kFewCols = 32, kFewWaves = 8;
 
-// The 32 bytes at p, or zeros.
-__device__ __forceinline__ v8i load32(const uint8_t* p, bool some) {
-    v4i lo = *reinterpret_cast<const v4i*>(p), hi = *reinterpret_cast<const v4i*>(p + 16);
-    return some ? __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7) : v8i{};
+// The 32 bytes at p + at of a row of len bytes (a multiple of 16, not 0), zeros
+// past its end.
+__device__ __forceinline__ v8i load32(const uint8_t* p, int64_t at, int64_t len) {
+    const bool first = at < len, second = at + 16 < len;
+    const v4i lo = *reinterpret_cast<const v4i*>(p + (first ? at : 0));
+    const v4i hi = *reinterpret_cast<const v4i*>(p + (second ? at + 16 : 0));
+    const v4i zero = {};
+    return __builtin_shufflevector(first ? lo : zero, second ? hi : zero, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 template <int BM, bool F32>
@@ -837,16 +841,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
         v8i fa[MT], fb[NT];
         float sa[MT], sb;
         auto fetch = [&](int k) {
-            // a lane's 32 bytes may end past the contraction (K is a multiple of
-            // 16): then it is read 16 bytes back, or not at all
             const int64_t at = (int64_t)k * kBK + fg * 32;
-            const bool some = at < p.K, half = at + 32 > p.K;
-            const int64_t from = some ? (half ? at - 16 : at) : 0;
-            auto get = [&](const uint8_t* q) {
-                v8i v = load32(q + from, some);
-                if (half && some) v = v8i{v[4], v[5], v[6], v[7], 0, 0, 0, 0};
-                return v;
-            };
+            auto get = [&](const uint8_t* q) { return load32(q, at, p.K); };
 #pragma unroll
             for (int j = 0; j < NT; ++j) fb[j] = get(pb[j]);
 #pragma unroll

@@ -746,15 +746,16 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     load_wait();            // no load into LDS is left behind
 }
 
-// ---- block128 for few rows a group -------------------------------------------
+// ---- few output rows, or few outputs of a long contraction -----------------------
 //
-// With a handful of rows the weights' bytes are the whole cost: a tile is BM
-// rows by 32 columns, and its eight waves take the contraction's blocks in turn
-// (wave w: w, w + 8, ...), so that even one small product has enough loads in
-// flight on every CU. Fragments come straight from memory, four lanes a line,
-// the next block's while this one is multiplied; sums are exact (the matrix
-// cores have nothing else to do). The waves' sums meet in LDS and are added in
-// wave order.
+// With a handful of rows the weights' bytes are block128's whole cost, and with a
+// small weight wgrad has few tiles of a long contraction: a tile is BM rows by 32
+// columns, and its eight waves take the contraction's blocks in turn (wave w: w,
+// w + 8, ...), so that even one small product has enough loads in flight on every
+// CU. Fragments come straight from memory, four lanes a line, the next block's
+// while this one is multiplied; sums are exact (the matrix cores have nothing else
+// to do). The waves' sums meet in LDS and are added in wave order. Bound by the
+// loads: one row by 8192 x 8192 17 us, 4 TB/s.
 constexpr int kFewCols = 32, kFewWaves = 8;
 
 // The 32 bytes at p + at of a row of len bytes (a multiple of 16, not 0), zeros
@@ -767,58 +768,80 @@ __device__ __forceinline__ v8i load32(const uint8_t* p, int64_t at, int64_t len)
     return __builtin_shufflevector(first ? lo : zero, second ? hi : zero, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int BM, bool F32>
+template <int BM, bool WGRAD, bool F32>
 __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     constexpr int MT = BM / 16, NT = kFewCols / 16;
     __shared__ __align__(16) float s_sum[kFewWaves][BM][kFewCols + 4];
     const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)(threadIdx.x / kWave));
-    const int nkb = (int)((p.K + kBK - 1) / kBK);
     const int64_t nnb = (p.N + 127) / 128;
-    const int col_tiles = (int)((p.N + kFewCols - 1) / kFewCols), M = (int)p.M;
+    const int col_tiles = (int)((p.cols + kFewCols - 1) / kFewCols), M = (int)p.M;
 
     // ---- which tile: every wave finds it, 64 groups at a time ----
+    constexpr int kAlign = WGRAD ? 16 : 1;
     int carry = 0, tiles = 0;
     int e = 0, b = 0;                      // this lane's group
     auto group = [&](int g, int from) {
         int raw = 0;
-        if (g < p.G) raw = p.offsets ? min(max(p.offsets[g], 0), M) : M;
+        if (g < p.G) raw = p.offsets ? min(max(p.offsets[g], 0), M) / kAlign * kAlign : M;
         e = max(wave_prefix_imax(raw), from);
         b = __shfl_up(e, 1, kWave);
         if (lane == 0) b = from;
         return wave_prefix_sum((e - b + BM - 1) / BM);
     };
-    int upto = 0;
-    for (int base = 0; base < p.G; base += kWave) {
-        upto = tiles + group(base + lane, carry);
-        tiles = uniform(__shfl(upto, kWave - 1, kWave));
-        carry = uniform(__shfl(e, kWave - 1, kWave));
-    }
-    const int last_end = carry, total = (tiles + (M - last_end + BM - 1) / BM) * col_tiles;
-    if ((int)blockIdx.x >= total) return;
-    const int L = tile_of(blockIdx.x, total);
-    int g = -1, begin = last_end, end = M, before = tiles;
-    if (L < tiles * col_tiles) {
-        if (p.G > kWave) {
-            carry = tiles = 0;
-            for (int base = 0;; base += kWave) {
-                upto = tiles + group(base + lane, carry);
-                g = base;
-                const int now = uniform(__shfl(upto, kWave - 1, kWave));
-                if (L < now * col_tiles) break;
-                tiles = now;
-                carry = uniform(__shfl(e, kWave - 1, kWave));
-            }
-        } else {
-            g = 0;
+    int g = -1, begin, end;                // the group and its rows, wgrad: its part of the contraction
+    int m0, n0;
+    if constexpr (WGRAD) {
+        const int row_tiles = (int)((p.N + BM - 1) / BM), per = row_tiles * col_tiles;
+        const int L = tile_of(blockIdx.x, p.G * per);
+        g = uniform(L / per);
+        for (int base = 0; base <= g; base += kWave) {
+            group(base + lane, carry);
+            carry = uniform(__shfl(e, kWave - 1, kWave));
         }
-        const int at = __builtin_ctzll(__ballot(upto * col_tiles > L));
-        g = uniform(g + at);
-        begin = uniform(__shfl(b, at, kWave));
-        end = uniform(__shfl(e, at, kWave));
-        before = uniform(__shfl(upto, at, kWave)) - (end - begin + BM - 1) / BM;
+        begin = uniform(__shfl(b, g % kWave, kWave));
+        end = uniform(__shfl(e, g % kWave, kWave));
+        m0 = uniform(L - g * per) % row_tiles * BM;
+        n0 = uniform(L - g * per) / row_tiles * kFewCols;
+    } else {
+        int upto = 0;
+        for (int base = 0; base < p.G; base += kWave) {
+            upto = tiles + group(base + lane, carry);
+            tiles = uniform(__shfl(upto, kWave - 1, kWave));
+            carry = uniform(__shfl(e, kWave - 1, kWave));
+        }
+        const int last_end = carry, total = (tiles + (M - last_end + BM - 1) / BM) * col_tiles;
+        if ((int)blockIdx.x >= total) return;
+        const int L = tile_of(blockIdx.x, total);
+        int before = tiles;
+        begin = last_end;
+        end = M;
+        if (L < tiles * col_tiles) {
+            if (p.G > kWave) {
+                carry = tiles = 0;
+                for (int base = 0;; base += kWave) {
+                    upto = tiles + group(base + lane, carry);
+                    g = base;
+                    const int now = uniform(__shfl(upto, kWave - 1, kWave));
+                    if (L < now * col_tiles) break;
+                    tiles = now;
+                    carry = uniform(__shfl(e, kWave - 1, kWave));
+                }
+            } else {
+                g = 0;
+            }
+            const int at = __builtin_ctzll(__ballot(upto * col_tiles > L));
+            g = uniform(g + at);
+            begin = uniform(__shfl(b, at, kWave));
+            end = uniform(__shfl(e, at, kWave));
+            before = uniform(__shfl(upto, at, kWave)) - (end - begin + BM - 1) / BM;
+        }
+        const int rows = (end - begin + BM - 1) / BM, local = L - before * col_tiles;
+        m0 = begin + local % rows * BM;
+        n0 = local / rows * kFewCols;
     }
-    const int rows = (end - begin + BM - 1) / BM, local = L - before * col_tiles;
-    const int m0 = begin + local % rows * BM, n0 = local / rows * kFewCols;
+    const int64_t row_end = WGRAD ? p.N : end;
+    const int64_t stride = WGRAD ? p.M : p.K, len = WGRAD ? end - begin : p.K;
+    const int nkb = (int)((len + kBK - 1) / kBK);
 
     // ---- the contraction ----
     const int fr = lane & 15, fg = lane / 16;
@@ -827,30 +850,33 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
-    if (g >= 0) {
+    if (g >= 0 && len > 0) {
         const uint8_t *pa[MT], *pb[NT];
         const float *psa[MT], *psb = p.b_scales + (g * nnb + n0 / 128) * nkb;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const int64_t r = min(m0 + i * 16 + fr, end - 1);
-            pa[i] = p.a + r * p.K;
+            const int64_t r = min((int64_t)m0 + i * 16 + fr, row_end - 1);
+            pa[i] = p.a + r * stride + (WGRAD ? begin : 0);
             psa[i] = p.a_scales + r * nkb;
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) pb[j] = p.b + (g * p.N + min((int64_t)n0 + j * 16 + fr, p.N - 1)) * p.K;
+        for (int j = 0; j < NT; ++j) {
+            const int64_t r = min((int64_t)n0 + j * 16 + fr, p.cols - 1);
+            pb[j] = WGRAD ? p.b + r * stride + begin : p.b + (g * p.N + r) * stride;
+        }
         v8i fa[MT], fb[NT];
         float sa[MT], sb;
         auto fetch = [&](int k) {
             const int64_t at = (int64_t)k * kBK + fg * 32;
-            auto get = [&](const uint8_t* q) { return load32(q, at, p.K); };
+            auto get = [&](const uint8_t* q) { return load32(q, at, len); };
 #pragma unroll
             for (int j = 0; j < NT; ++j) fb[j] = get(pb[j]);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 fa[i] = get(pa[i]);
-                sa[i] = psa[i][k];
+                if constexpr (!WGRAD) sa[i] = psa[i][k];
             }
-            sb = psb[k];
+            if constexpr (!WGRAD) sb = psb[k];
         };
         if (wave < nkb) fetch(wave);
         for (int k = wave; k < nkb; k += kFewWaves) {
@@ -861,7 +887,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 na[i] = fa[i];
-                f[i] = (1.0f / sa[i]) * (1.0f / sb);
+                if constexpr (!WGRAD) f[i] = (1.0f / sa[i]) * (1.0f / sb);
             }
             if (k + kFewWaves < nkb) fetch(k + kFewWaves);
             using Op = Operand<false>;
@@ -870,6 +896,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
             for (int j = 0; j < NT; ++j) ob[j] = Op(nb[j]);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
+                if constexpr (WGRAD) {
+                    Op::mfma(ob, Op(na[i]), acc[i]);
+                    continue;
+                }
                 v4f part[NT] = {};
                 Op::mfma(ob, Op(na[i]), part);
 #pragma unroll
@@ -889,11 +919,20 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     __syncthreads();
     for (int x = threadIdx.x; x < BM * kFewCols / 4; x += kFewWaves * 64) {
         const int r = x / (kFewCols / 4), c = x % (kFewCols / 4) * 4;
-        if (m0 + r >= end || n0 + c >= p.N) continue;
+        if (m0 + r >= row_end || n0 + c >= p.cols) continue;
         v4f v = *reinterpret_cast<const v4f*>(&s_sum[0][r][c]);
 #pragma unroll
         for (int w = 1; w < kFewWaves; ++w) v += *reinterpret_cast<const v4f*>(&s_sum[w][r][c]);
-        const int64_t at = (int64_t)(m0 + r) * p.N + n0 + c;
+        int64_t at = (int64_t)(m0 + r) * p.cols + n0 + c;
+        if constexpr (WGRAD) {
+            at += g * p.N * p.cols;
+            if (len > 0) {
+                const float ia = 1.0f / p.a_scales[(int64_t)(m0 + r) * p.G + g];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = v[i] * ia * (1.0f / p.b_scales[(int64_t)(n0 + c + i) * p.G + g]);
+            }
+            if (F32 && p.accumulate) v += *reinterpret_cast<const v4f*>(static_cast<const float*>(p.out) + at);
+        }
         if constexpr (F32)
             *reinterpret_cast<v4f*>(static_cast<float*>(p.out) + at) = v;
         else
@@ -902,15 +941,16 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     }
 }
 
-template <int BM>
+template <int BM, bool WGRAD>
 hipError_t launch_few(const MmArgs& p, bool f32, hipStream_t stream) {
-    const int64_t groups = p.offsets ? p.G + 1 : 1;
-    const int64_t blocks = (p.M + (groups < p.M ? groups : p.M) * (BM - 1)) / BM * ((p.N + kFewCols - 1) / kFewCols);
+    const int64_t groups = p.offsets ? p.G + 1 : 1, spare = groups < p.M ? groups : p.M;
+    const int64_t down = WGRAD ? p.G * ((p.N + BM - 1) / BM) : (p.M + spare * (BM - 1)) / BM;
+    const int64_t blocks = down * ((p.cols + kFewCols - 1) / kFewCols);
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
     if (f32)
-        hipLaunchKernelGGL((mm_few_kernel<BM, true>), dim3((unsigned)blocks), dim3(kFewWaves * 64), 0, stream, p);
+        hipLaunchKernelGGL((mm_few_kernel<BM, WGRAD, true>), dim3((unsigned)blocks), dim3(kFewWaves * 64), 0, stream, p);
     else
-        hipLaunchKernelGGL((mm_few_kernel<BM, false>), dim3((unsigned)blocks), dim3(kFewWaves * 64), 0, stream, p);
+        hipLaunchKernelGGL((mm_few_kernel<BM, WGRAD, false>), dim3((unsigned)blocks), dim3(kFewWaves * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -941,28 +981,39 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   33 on tiles); up to 40 rows two, and four where that is at most one
 //   workgroup a CU (64 rows by 8192 x 8192: 39 and 66; 256 rows by 4096 x 4096,
 //   two a CU: 36 and 32).
+// - few outputs of wgrad: the same form with the fewest rows a tile that still
+//   leaves one workgroup a CU (16640 x 256 x 272: 25 with 16 rows, 48 with 64, and
+//   66 on tiles of 128 x 128 in two parts; 16384 x 1024 x 512: 48 and 60, twice as
+//   many outputs 93 and 61; with binary32 sums still 93 and 94, and 43 and 52 in
+//   four groups of 512 x 512).
 // - 256 x 256 tiles where they fill the CUs, twice if groups end inside them
-//   (block128 16640 x 5120 x 8192 in 16 groups: 822, and 1005 with 128 x 128;
-//   2048 x 4096 x 4096, half the CUs: 66 and 48) and, for wgrad, where the contraction is long or the tiles are many
-//   (16640 x 8192 x 5120 in 16 groups: 839 and 948; 4096 x 2048 x 2048 in 8
-//   groups, four steps a tile: 40 and 32).
+//   (block128 16640 x 5120 x 8192 in 16 groups: 780, and about 1000 with 128 x
+//   128; 2048 x 4096 x 4096, half the CUs: 66 and 48) and, for wgrad, where the
+//   contraction is long or the tiles are many (16640 x 8192 x 5120 in 16 groups:
+//   745, and about 950; 4096 x 2048 x 2048 in 8 groups, four steps a tile: 40 and
+//   32).
 // - 128 x 128 tiles otherwise, two workgroups a CU (block128 with binary32 sums
-//   has no registers for more: 256 x 128 took 1591, 128 x 128 1491); where they
-//   leave half the CUs idle, two sets of waves share a tile's contraction (256 x
-//   4096 x 4096: 32 to 27; wgrad 8192 x 1024 x 1024: 44 to 37; with binary32 sums
-//   block128 does not gain).
+//   has no registers for more: 256 x 128 took 1591, 128 x 128 1491; 128 x 64,
+//   three a CU, did not gain on 1003 x 4176 x 4112, and lost a third on
+//   8192 x 8192 x 4096); where they leave half the CUs idle, two sets of waves
+//   share a tile's contraction (256 x 4096 x 4096: 27 to 22; wgrad 8192 x 1024 x
+//   1024 in two groups: 44 to 37; with binary32 sums block128 does not gain).
 template <bool WGRAD, bool FAST>
 hipError_t launch_sized(const MmArgs& p, bool f32, int cus, hipStream_t stream) {
     const int64_t groups = p.offsets ? p.G : 1;
     if constexpr (WGRAD) {
+        const int64_t across = groups * up(p.K, kFewCols);
+        if (across * up(p.N, 16) <= cus) return launch_few<16, true>(p, f32, stream);
+        if (across * up(p.N, 32) <= cus) return launch_few<32, true>(p, f32, stream);
+        if (across * up(p.N, 64) <= (FAST ? cus : 2 * cus)) return launch_few<64, true>(p, f32, stream);
         const int64_t tiles = groups * up(p.N, 256) * up(p.K, 256);
         if (tiles >= cus && (p.M / groups >= 2048 || tiles >= 4 * cus))
             return launch<256, 256, 128, 64, 1, true, FAST>(p, f32, cus, stream);
     } else {
         const int64_t rows = up(p.M, groups);
-        if (rows <= 20) return launch_few<16>(p, f32, stream);
-        if (groups == 1 && rows <= 40) return launch_few<32>(p, f32, stream);
-        if (groups == 1 && up(p.M, 64) * up(p.N, kFewCols) <= cus) return launch_few<64>(p, f32, stream);
+        if (rows <= 20) return launch_few<16, false>(p, f32, stream);
+        if (groups == 1 && rows <= 40) return launch_few<32, false>(p, f32, stream);
+        if (groups == 1 && up(p.M, 64) * up(p.N, kFewCols) <= cus) return launch_few<64, false>(p, f32, stream);
         if constexpr (FAST) {
             if ((up(p.M, 256) + groups / 2) * up(p.N, 256) >= (groups == 1 ? cus : 2 * cus))
                 return launch<256, 256, 128, 64, 1, false, true>(p, f32, cus, stream);

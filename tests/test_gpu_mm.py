@@ -226,3 +226,13 @@ def test_past_two_to_the_31_elements():
     dw = mgs.mgs_mm_wgrad(to_dev(codes(rng, (N, 32))), torch.ones((N, G), device=dev()), to_dev(codes(rng, (K, 32))),
                           torch.ones((K, G), device=dev()), to_dev(np.array([0] * 8 + [32], np.int32)), torch.bfloat16)
     assert dw.numel() > 1 << 31 and (dw[:8, ::997, ::31] == 0).all() and (dw[8] != 0).any(1).all()
+
+
+@pytest.mark.parametrize("M,N,K,G,kind", [
+    (640, 400, 400, 1, "even"), (1120, 16, 16, 70, "tail"), (4112, 48, 32, 3, "bad"), (16, 16, 16, 1, "even"),
+    (2048, 272, 272, 2, "one"), (336, 32, 48, 130, "tail"), (1296, 528, 496, 1, "tail")])
+@pytest.mark.parametrize("out", ["bf16", "f32", "accumulate"])
+@pytest.mark.parametrize("fast", [False, True])
+def test_mm_wgrad_of_few_outputs(M, N, K, G, kind, out, fast):
+    """Weights so small that each workgroup takes a group's whole contraction."""
+    test_mm_wgrad(M, N, K, G, kind, out, fast)

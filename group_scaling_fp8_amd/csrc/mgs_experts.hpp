@@ -23,7 +23,6 @@ struct DispatchArgs {
     uint8_t* q;             // (P, D) E4M3 or null
     float* scales;          // (P, ceil(D / 128))
     int32_t* hist;          // workspace: slot counts (moe_runs, E), or null
-    bool wide;              // 16-byte stores of q (set by launch_dispatch)
 };
 
 // An upper bound on the rows that the experts' groups take (a multiple of align).

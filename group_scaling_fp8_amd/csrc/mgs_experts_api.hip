@@ -69,7 +69,7 @@ int mgs_moe_dispatch(const void* x, int64_t T, int64_t D, const int32_t* expert_
     const mgs::DispatchArgs a{static_cast<const uint16_t*>(x), expert_ids, T, moves ? D : 0, top_k, n_experts, align,
                               n_rows, (flags & MGS_FLAG_POW2_SCALE) ? 1 : 0, offsets, rows, slots,
                               moves ? static_cast<uint16_t*>(xp) : nullptr, moves ? static_cast<uint8_t*>(q) : nullptr,
-                              scales, static_cast<int32_t*>(workspace), false};
+                              scales, static_cast<int32_t*>(workspace)};
     return hip_status(mgs::launch_dispatch(a, mgs::device_cus(), as_stream(stream)));
 }
 

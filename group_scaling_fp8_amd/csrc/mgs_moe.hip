@@ -161,34 +161,19 @@ __global__ __launch_bounds__(WAVES * 64) void rank_kernel(DispatchArgs a, int64_
 
 constexpr int kDispatchThreads = 256;
 constexpr int kDispatchWaves = kDispatchThreads / kWave;
-constexpr int kUnit = 1024;              // columns of a wave's piece: 16 a lane, eight lanes a block of 128
+constexpr int kUnit = 1024;              // columns of a wave's piece: two halves of eight a lane, 16 lanes a block of 128
 
-// Max over groups of eight lanes, in every lane of them.
-__device__ __forceinline__ uint32_t row8_max(uint32_t v) {
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));     // lane ^ 1
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));     // lane ^ 2
-    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));    // 7 - lane
-    return v;
+__device__ __forceinline__ int64_t column(int u, int h) {
+    return (int64_t)u * kUnit + h * (kUnit / 2) + (threadIdx.x & (kWave - 1)) * 8;
 }
 
-// 16 columns of row p: `half` when only the first eight exist. Rows whose
-// length is an odd multiple of 8 are not 16-byte aligned.
-__device__ __forceinline__ void put(const DispatchArgs& a, int64_t p, int64_t col, bool half, const uint4 (&x)[2],
-                                    uint4 q, float scale) {
-    if (a.xp) {
-        uint16_t* o = a.xp + p * a.D + col;
-        store_stream16(o, x[0]);
-        if (!half) store_stream16(o + 8, x[1]);
-    }
+// Eight columns of row p. A wave's stores are whole lines: with 16 columns a lane,
+// every second 16 bytes a store, xp came at half the rate.
+__device__ __forceinline__ void put(const DispatchArgs& a, int64_t p, int64_t col, uint4 x, uint2 q, float scale) {
+    if (a.xp) store_stream16(a.xp + p * a.D + col, x);
     if (a.q) {
-        uint8_t* o = a.q + p * a.D + col;
-        if (a.wide) {
-            store_stream16(o, q);
-        } else {
-            store_stream(o, make_uint2(q.x, q.y));
-            if (!half) store_stream(o + 8, make_uint2(q.z, q.w));
-        }
-        if ((threadIdx.x & 7) == 0) a.scales[p * ((a.D + 127) / 128) + col / 128] = scale;
+        store_stream(a.q + p * a.D + col, q);
+        if ((threadIdx.x & 15) == 0) a.scales[p * ((a.D + 127) / 128) + col / 128] = scale;
     }
 }
 
@@ -196,30 +181,37 @@ __device__ __forceinline__ void put(const DispatchArgs& a, int64_t p, int64_t co
 // scale of an empty block.
 __device__ __forceinline__ void zero_row(const DispatchArgs& a, int64_t p, int u0, int ustep, int units) {
     const float scale = group_scale(0u, a.pow2 != 0);
-    const uint4 zero[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    for (int u = u0; u < units; u += ustep) {
-        const int64_t col = (int64_t)u * kUnit + (threadIdx.x & (kWave - 1)) * 16;
-        if (col < a.D) put(a, p, col, col + 8 >= a.D, zero, zero[0], scale);
-    }
+    for (int u = u0; u < units; u += ustep)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (column(u, h) < a.D) put(a, p, column(u, h), make_uint4(0, 0, 0, 0), make_uint2(0, 0), scale);
 }
 
-// Unit u of token t: 16 columns a lane, zeros past the end.
+// Unit u of token t, zeros past its end.
 __device__ __forceinline__ void load_piece(const DispatchArgs& a, int64_t t, int u, uint4 (&x)[2]) {
-    const int64_t col = (int64_t)u * kUnit + (threadIdx.x & (kWave - 1)) * 16;
-    const uint16_t* src = a.x + t * a.D + col;
-    x[0] = x[1] = make_uint4(0, 0, 0, 0);
-    if (col < a.D) x[0] = *reinterpret_cast<const uint4*>(src);
-    if (col + 8 < a.D) x[1] = *reinterpret_cast<const uint4*>(src + 8);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        x[h] = make_uint4(0, 0, 0, 0);
+        if (column(u, h) < a.D) x[h] = *reinterpret_cast<const uint4*>(a.x + t * a.D + column(u, h));
+    }
 }
 
 // Its cast, made once, to the rows of the token's k slots.
 __device__ __forceinline__ void put_piece(const DispatchArgs& a, const int* rows, int u, const uint4 (&x)[2]) {
-    const int64_t col = (int64_t)u * kUnit + (threadIdx.x & (kWave - 1)) * 16;
-    const float s = group_scale(row8_max(mag_fold(mag_max8(mag_max8(0u, x[0]), x[1]))), a.pow2 != 0);
-    const uint2 lo = cast8_group(x[0], s), hi = cast8_group(x[1], s);
-    if (col >= a.D) return;
-    for (int j = 0; j < a.k; ++j)
-        if (rows[j] >= 0) put(a, rows[j], col, col + 8 >= a.D, x, make_uint4(lo.x, lo.y, hi.x, hi.y), s);
+    float s[2];
+    uint2 q[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        s[h] = group_scale(row16_max(mag_fold(mag_max8(0u, x[h]))), a.pow2 != 0);
+        q[h] = cast8_group(x[h], s[h]);
+    }
+    for (int j = 0; j < a.k; ++j) {
+        const int row = rows[j];
+        if (row < 0) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (column(u, h) < a.D) put(a, row, column(u, h), x[h], q[h], s[h]);
+    }
 }
 
 // Everything in one launch, for few slots: workgroups below `groups` take `per`
@@ -437,9 +429,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(
 
 }  // namespace
 
-hipError_t launch_dispatch(const DispatchArgs& args, int cus, hipStream_t stream) {
-    DispatchArgs a = args;
-    a.wide = a.D % 16 == 0 && (reinterpret_cast<uintptr_t>(a.q) & 15) == 0;
+hipError_t launch_dispatch(const DispatchArgs& a, int cus, hipStream_t stream) {
     const int64_t n = a.T * a.k, units = (a.D + kUnit - 1) / kUnit;
     const bool moves = a.xp || a.q;
     if (n <= kMoeFusedSlots) {

@@ -147,7 +147,8 @@ int mgs_mm_block128(const void* a, const float* a_scales, int64_t M, int64_t K, 
     if ((M / 16 + n_groups + 1) * ((N + 15) / 16) > INT32_MAX) return MGS_ERR_UNSUPPORTED;
     return hip_status(mgs::launch_mm_block128(static_cast<const uint8_t*>(a), a_scales, M, K,
                                               static_cast<const uint8_t*>(b), b_scales, n_groups, N, offsets,
-                                              (flags & MGS_FLAG_FAST_ACCUM) != 0, out_type == MGS_OUT_F32, y, mgs::device_cus(), as_stream(stream)));
+                                              (flags & MGS_FLAG_FAST_ACCUM) != 0, out_type == MGS_OUT_F32, y,
+                                              mgs::device_cus(), as_stream(stream)));
 }
 
 int mgs_mm_wgrad(const void* a_t, const float* a_scales_t, const void* b_t, const float* b_scales_t, int64_t M,
@@ -167,7 +168,8 @@ int mgs_mm_wgrad(const void* a_t, const float* a_scales_t, const void* b_t, cons
     return hip_status(mgs::launch_mm_wgrad(static_cast<const uint8_t*>(a_t), a_scales_t,
                                            static_cast<const uint8_t*>(b_t), b_scales_t, M, N, K, offsets, n_groups,
                                            (flags & MGS_FLAG_FAST_ACCUM) != 0, out_type == MGS_OUT_F32,
-                                           (flags & MGS_FLAG_ACCUMULATE) != 0, dw, mgs::device_cus(), as_stream(stream)));
+                                           (flags & MGS_FLAG_ACCUMULATE) != 0, dw, mgs::device_cus(),
+                                           as_stream(stream)));
 }
 
 }  // extern "C"

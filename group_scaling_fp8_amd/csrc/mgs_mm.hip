@@ -134,7 +134,8 @@ struct Loads {
     uint32_t voff, step, lds;        // of the lane's first row, to the next load's, of the wave's first line
     bool inside;
 
-    __device__ __forceinline__ Loads(v4i src, uint32_t voff, uint32_t step, int chunk, int kk, int len, int skip, uint32_t lds)
+    __device__ __forceinline__ Loads(v4i src, uint32_t voff, uint32_t step, int chunk, int kk, int len, int skip,
+                                     uint32_t lds)
         : src(src), step(step), lds(lds) {
 #ifdef __HIP_DEVICE_COMPILE__
         asm volatile("" : "+s"(kk));        // offsets are made here, not kept in registers for each kk
@@ -303,6 +304,8 @@ __device__ __forceinline__ void wait_some_or_none(int some) {
 //   exact             block128 1080 TFLOP/s, wgrad 1580: the bf16 instructions
 //                     take twice the cycles, and every wave widens the bytes of
 //                     its fragments itself, which takes issue slots.
+//                     (Under these loads the card lowers its clock to 2.0 GHz, and
+//                     to 1.7 where the matrix cores are busy nine cycles in ten.)
 //   few tiles         latency: two steps' loads (64 KiB a CU) are in flight, and a
 //                     CU takes in 35 to 45 KB/us whatever the form.
 template <int BM, int BN, int WM, int WN, int PARTS, bool WGRAD, bool FAST, bool F32>
@@ -318,7 +321,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     // of each) and columns; wgrad: the scales of the last, this and the next
     // tile's rows and columns
     __shared__ __align__(16) float s_all_scale[PARTS][(WGRAD ? 3 : 4) * WAVES * 64];
-    __shared__ float s_all_raw[PARTS][2][WGRAD ? 1 : WAVES * 64];     // block128: the scale each thread fetches, of two steps
+    // block128: the scale each thread fetches, of two steps
+    __shared__ float s_all_raw[PARTS][2][WGRAD ? 1 : WAVES * 64];
     __shared__ Groups s_groups;
     const int lane = threadIdx.x & (kWave - 1);
     const int part_of = PARTS > 1 ? uniform((int)(threadIdx.x / (WAVES * kWave))) : 0;
@@ -699,7 +703,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
     if constexpr (WGRAD) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            ib[j] = *reinterpret_cast<const v4f*>(scale + BM + wn + (F32 ? j * 16 + fg * 4 : (j >> 1) * 32 + fg * 8 + (j & 1) * 4));
+            ib[j] = *reinterpret_cast<const v4f*>(
+                scale + BM + wn + (F32 ? j * 16 + fg * 4 : (j >> 1) * 32 + fg * 8 + (j & 1) * 4));
 #pragma unroll
             for (int c = 0; c < 4; ++c) ib[j][c] = 1.0f / ib[j][c];
         }

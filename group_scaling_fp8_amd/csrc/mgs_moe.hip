@@ -8,7 +8,7 @@
 // result is the same on every run.
 //
 // All of it is bound by memory traffic, and with few tokens by a launch's fixed
-// cost. Times here are of single launches on MI355X with cold caches.
+// cost. Times are of MI355X.
 #include "mgs_block128_device.hpp"
 #include "mgs_experts.hpp"
 
@@ -231,7 +231,8 @@ __global__ __launch_bounds__(kFusedThreads) void dispatch_fused_kernel(DispatchA
     const int n = (int)(a.T * k), t0 = blockIdx.x * per;
     const int tokens = (int)blockIdx.x < groups ? min(per, (int)a.T - t0) : 0;
     const int first = tokens ? t0 * k : n, last = first + tokens * k;
-    const int units = (int)((a.D + kUnit - 1) / kUnit), u0 = blockIdx.y, mine = (units - u0 + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int units = (int)((a.D + kUnit - 1) / kUnit), u0 = blockIdx.y;
+    const int mine = (units - u0 + (int)gridDim.y - 1) / (int)gridDim.y;
     // a wave's pieces: (token, unit) pairs of this workgroup, one in kFusedWaves
     const int pieces = tokens * mine;
     auto unit_of = [&](int i) { return u0 + i % mine * (int)gridDim.y; };

@@ -5,6 +5,12 @@ already be on the GPU; bf16 tensors may be torch.bfloat16, int16 or
 uint16 (the raw bit patterns are used). Outputs come back as torch.uint8
 (E4M3 bytes; ``.view(torch.float8_e4m3fn)`` reinterprets them), float32
 scales, and uint8 E8M0 scales.
+
+With ``stream`` a call runs there instead of on the current stream: the
+caller orders that stream behind the work that makes the inputs (and behind
+the last use of outputs it passes), keeps them until the call has run, and
+orders its own use of the outputs behind the call. Outputs that a call
+allocates are ``stream``'s memory and need no care beyond that.
 """
 from __future__ import annotations
 
@@ -49,9 +55,32 @@ def _need(t: torch.Tensor, name: str, dtypes, ndim: Optional[int] = None):
 _U8_LIKE = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _out(t, shape, dtype, device, name):
+def _allocator(stream, device):
+    """torch.empty for what a call on `stream` writes. With a stream other than
+    the current one it takes that stream's memory: the current stream's may
+    still be read by work queued there, and once freed could be handed out
+    there before the call has run. The tensor is recorded on the current
+    stream, where the caller uses it."""
+    if stream is None:
+        return torch.empty
+    current = torch.cuda.current_stream(device)
+    handle = _stream_handle(stream)
+    if handle == current.cuda_stream:
+        return torch.empty
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=device)
+
+    def empty(shape, dtype, device):
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        t.record_stream(current)
+        return t
+    return empty
+
+
+def _out(t, shape, dtype, device, name, stream=None):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _allocator(stream, device)(shape, dtype=dtype, device=device)
     _need(t, name, (dtype,) if dtype != torch.uint8 else _U8_LIKE)
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
@@ -102,8 +131,8 @@ def mgs_quant_groups_dim0(x: torch.Tensor, offsets: torch.Tensor, pow2: bool = F
     _need(offsets, "offsets", (torch.int32,), 1)
     M, K = x.shape
     G = offsets.shape[0]
-    q = _out(q, (M, K), torch.uint8, x.device, "q")
-    scales = _out(scales, (G, K), torch.float32, x.device, "scales")
+    q = _out(q, (M, K), torch.uint8, x.device, "q", stream)
+    scales = _out(scales, (G, K), torch.float32, x.device, "scales", stream)
     if workspace is None:
         st = lib().mgs_quant_groups_dim0(x.data_ptr(), M, K, offsets.data_ptr(), G,
                                          _flags(pow2, validate), q.data_ptr(),
@@ -129,8 +158,8 @@ def mgs_quant_groups_dim0_noalloc(x: torch.Tensor, offsets: torch.Tensor, pow2: 
     _need(offsets, "offsets", (torch.int32,), 1)
     M, K = x.shape
     G = offsets.shape[0]
-    q = _out(q, (M, K), torch.uint8, x.device, "q")
-    scales = _out(scales, (G, K), torch.float32, x.device, "scales")
+    q = _out(q, (M, K), torch.uint8, x.device, "q", stream)
+    scales = _out(scales, (G, K), torch.float32, x.device, "scales", stream)
     st = lib().mgs_quant_groups_dim0_noalloc(x.data_ptr(), M, K, offsets.data_ptr(), G,
                                              _flags(pow2, validate), q.data_ptr(),
                                              scales.data_ptr(), _stream_handle(stream, x))
@@ -150,8 +179,8 @@ def mgs_quant_groups_dim0_t(x: torch.Tensor, offsets: torch.Tensor, pow2: bool =
     _need(offsets, "offsets", (torch.int32,), 1)
     M, K = x.shape
     G = offsets.shape[0]
-    q_t = _out(q_t, (K, M), torch.uint8, x.device, "q_t")
-    scales_t = _out(scales_t, (K, G), torch.float32, x.device, "scales_t")
+    q_t = _out(q_t, (K, M), torch.uint8, x.device, "q_t", stream)
+    scales_t = _out(scales_t, (K, G), torch.float32, x.device, "scales_t", stream)
     wp, wb = _ws_args(workspace)
     st = lib().mgs_quant_groups_dim0_t(x.data_ptr(), M, K, offsets.data_ptr(), G,
                                        _flags(pow2, validate), q_t.data_ptr(),
@@ -167,8 +196,8 @@ def mgs_quant_experts_dim1(w: torch.Tensor, pow2: bool = False, q: Optional[torc
     Returns q (E, D1, D2) uint8 E4M3 and scales (E, D2) float32."""
     _need(w, "w", _BF16_LIKE, 3)
     E, D1, D2 = w.shape
-    q = _out(q, (E, D1, D2), torch.uint8, w.device, "q")
-    scales = _out(scales, (E, D2), torch.float32, w.device, "scales")
+    q = _out(q, (E, D1, D2), torch.uint8, w.device, "q", stream)
+    scales = _out(scales, (E, D2), torch.float32, w.device, "scales", stream)
     wp, wb = _ws_args(workspace)
     st = lib().mgs_quant_experts_dim1(w.data_ptr(), E, D1, D2, MGS_FLAG_POW2_SCALE if pow2 else 0,
                                       q.data_ptr(), scales.data_ptr(), wp, wb, _stream_handle(stream, w))
@@ -185,8 +214,8 @@ def mgs_quant_groups_dim1(x: torch.Tensor, offsets: torch.Tensor, pow2: bool = F
     _need(offsets, "offsets", (torch.int32,), 1)
     M, K = x.shape
     G = offsets.shape[0]
-    q = _out(q, (M, K), torch.uint8, x.device, "q")
-    scales = _out(scales, (M, G), torch.float32, x.device, "scales")
+    q = _out(q, (M, K), torch.uint8, x.device, "q", stream)
+    scales = _out(scales, (M, G), torch.float32, x.device, "scales", stream)
     st = lib().mgs_quant_groups_dim1(x.data_ptr(), M, K, offsets.data_ptr(), G,
                                      _flags(pow2, validate), q.data_ptr(),
                                      scales.data_ptr(), _stream_handle(stream, x))
@@ -205,8 +234,8 @@ def mgs_mx_quant_dim0(x: torch.Tensor, mode: int = MGS_MX_FLOOR,
     if mode not in (MGS_MX_FLOOR, MGS_MX_RCEIL):
         raise ValueError("mode must be MGS_MX_FLOOR or MGS_MX_RCEIL")
     M, K = x.shape
-    q = _out(q, (M, K), torch.uint8, x.device, "q")
-    scales = _out(scales, (M, K // 32), torch.uint8, x.device, "scales")
+    q = _out(q, (M, K), torch.uint8, x.device, "q", stream)
+    scales = _out(scales, (M, K // 32), torch.uint8, x.device, "scales", stream)
     off_ptr, G = (None, 0)
     if offsets is not None:
         _need(offsets, "offsets", (torch.int32,), 1)
@@ -225,8 +254,8 @@ def mgs_mx_quant_dim1(x: torch.Tensor, mode: int = MGS_MX_FLOOR, q_t: Optional[t
     E8M0 -- mgs_mx_quant_dim0 of x^T."""
     _need(x, "x", _BF16_LIKE, 2)
     M, K = x.shape
-    q_t = _out(q_t, (K, M), torch.uint8, x.device, "q_t")
-    scales_t = _out(scales_t, (K, M // 32), torch.uint8, x.device, "scales_t")
+    q_t = _out(q_t, (K, M), torch.uint8, x.device, "q_t", stream)
+    scales_t = _out(scales_t, (K, M // 32), torch.uint8, x.device, "scales_t", stream)
     st = lib().mgs_mx_quant_dim1(x.data_ptr(), M, K, int(mode), q_t.data_ptr(), scales_t.data_ptr(),
                                  _stream_handle(stream, x))
     check("mgs_mx_quant_dim1", st)
@@ -244,7 +273,7 @@ def mgs_mx_dequant_dim0(q: torch.Tensor, scales: torch.Tensor, y: Optional[torch
     if tuple(scales.shape) != (M, K // 32):
         raise ValueError("scales has shape %s, expected %s" % (tuple(scales.shape), (M, K // 32)))
     if y is None:
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
+        y = _allocator(stream, q.device)((M, K), dtype=torch.bfloat16, device=q.device)
     else:
         _need(y, "y", _BF16_LIKE, 2)
         if tuple(y.shape) != (M, K):
@@ -259,7 +288,7 @@ def mgs_cast_e4m3(x: torch.Tensor, out: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """E4M3 cast of a float32 tensor (numel % 4 == 0) with the library's cast."""
     _need(x, "x", (torch.float32,))
-    out = _out(out, tuple(x.shape), torch.uint8, x.device, "out")
+    out = _out(out, tuple(x.shape), torch.uint8, x.device, "out", stream)
     st = lib().mgs_cast_e4m3(x.data_ptr(), x.numel(), out.data_ptr(), _stream_handle(stream, x))
     check("mgs_cast_e4m3", st)
     return out

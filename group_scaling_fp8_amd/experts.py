@@ -25,7 +25,7 @@ import torch
 
 from ._lib import (MGS_ERR_INVALID_ARG, MGS_FLAG_ACCUMULATE, MGS_FLAG_FAST_ACCUM, MGS_FLAG_POW2_SCALE, MGS_OUT_BF16,
                    MGS_OUT_F32, MgsError, check, lib)
-from .api import _BF16_LIKE, _U8_LIKE, _need, _out, _stream_handle
+from .api import _BF16_LIKE, _U8_LIKE, _allocator, _need, _out, _stream_handle
 
 _OUT_TYPES = {torch.bfloat16: MGS_OUT_BF16, torch.float32: MGS_OUT_F32}
 
@@ -63,18 +63,6 @@ def mgs_moe_rows(T: int, top_k: int, n_experts: int, align: int = 16) -> int:
     return _order_sizes(int(T), int(top_k), int(n_experts), int(align))[0]
 
 
-def _workspace(need: int, device, stream) -> torch.Tensor:
-    """Workspace of one call, freed when the call returns: from the memory of
-    the stream that the call runs on, so that only later work on that stream
-    can be given it while the kernels still run."""
-    if stream is None:
-        return torch.empty((need,), dtype=torch.uint8, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_handle(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty((need,), dtype=torch.uint8, device=device)
-
-
 def _dispatch(x, ids, n_experts, align, pow2, cast, permuted, stream):
     _need(ids, "expert_ids", (torch.int32,), 2)
     T, k = ids.shape
@@ -88,17 +76,18 @@ def _dispatch(x, ids, n_experts, align, pow2, cast, permuted, stream):
         if x.shape[0] != T:
             raise ValueError("x has %d tokens, expert_ids %d" % (x.shape[0], T))
         D = x.shape[1]
-    offsets = torch.empty((E,), dtype=torch.int32, device=dev)
-    rows = torch.empty((T, k), dtype=torch.int32, device=dev)
-    slots = torch.empty((P,), dtype=torch.int32, device=dev)
+    empty = _allocator(stream, dev)
+    offsets = empty((E,), dtype=torch.int32, device=dev)
+    rows = empty((T, k), dtype=torch.int32, device=dev)
+    slots = empty((P,), dtype=torch.int32, device=dev)
     q = scales = xp = ws = None
     if cast:
-        q = torch.empty((P, D), dtype=torch.uint8, device=dev)
-        scales = torch.empty((P, (D + 127) // 128), dtype=torch.float32, device=dev)
+        q = empty((P, D), dtype=torch.uint8, device=dev)
+        scales = empty((P, (D + 127) // 128), dtype=torch.float32, device=dev)
     if permuted:
-        xp = torch.empty((P, D), dtype=torch.bfloat16, device=dev)
+        xp = empty((P, D), dtype=torch.bfloat16, device=dev)
     if need:
-        ws = _workspace(need, dev, stream)
+        ws = empty((need,), dtype=torch.uint8, device=dev)
     moves = P > 0 and D > 0
     st = lib().mgs_moe_dispatch(_ptr(x) if moves else None, T, D, ids.data_ptr(), k, E, align,
                                 MGS_FLAG_POW2_SCALE if pow2 else 0, P, offsets.data_ptr(), rows.data_ptr(),
@@ -136,7 +125,7 @@ def mgs_moe_combine(yp: torch.Tensor, rows: torch.Tensor, weights: Optional[torc
     T, k = rows.shape
     if weights is not None:
         _input(weights, yp, "weights", (torch.float32,), (T, k))
-    y = _out(y, (T, D), torch.bfloat16, yp.device, "y")
+    y = _out(y, (T, D), torch.bfloat16, yp.device, "y", stream)
     st = lib().mgs_moe_combine(yp.data_ptr(), P, D, rows.data_ptr(), T, k, _ptr(weights), y.data_ptr(),
                                _stream_handle(stream, yp))
     check("mgs_moe_combine", st)
@@ -159,8 +148,8 @@ def mgs_moe_combine_grad(dy: torch.Tensor, yp: torch.Tensor, rows: torch.Tensor,
     _input(yp, dy, "yp", _BF16_LIKE, (P, D))
     _input(slots, dy, "slots", (torch.int32,), (P,))
     _input(weights, dy, "weights", (torch.float32,), (T, k))
-    dyp = _out(dyp, (P, D), torch.bfloat16, dy.device, "dyp")
-    dw = _out(dw, (T, k), torch.float32, dy.device, "dw")
+    dyp = _out(dyp, (P, D), torch.bfloat16, dy.device, "dyp", stream)
+    dw = _out(dw, (T, k), torch.float32, dy.device, "dw", stream)
     st = lib().mgs_moe_combine_grad(dy.data_ptr(), yp.data_ptr(), P, D, rows.data_ptr(), slots.data_ptr(), T, k,
                                     weights.data_ptr(), dyp.data_ptr(), dw.data_ptr(), _stream_handle(stream, dy))
     check("mgs_moe_combine_grad", st)
@@ -173,8 +162,8 @@ def mgs_quant_rows128(x: torch.Tensor, pow2: bool = False, q: Optional[torch.Ten
     Returns q (M, K) uint8 E4M3 and scales (M, ceil(K/128)) float32."""
     _need(x, "x", _BF16_LIKE, 2)
     M, K = x.shape
-    q = _out(q, (M, K), torch.uint8, x.device, "q")
-    scales = _out(scales, (M, (K + 127) // 128), torch.float32, x.device, "scales")
+    q = _out(q, (M, K), torch.uint8, x.device, "q", stream)
+    scales = _out(scales, (M, (K + 127) // 128), torch.float32, x.device, "scales", stream)
     st = lib().mgs_quant_rows128(x.data_ptr(), M, K, MGS_FLAG_POW2_SCALE if pow2 else 0, q.data_ptr(),
                                  scales.data_ptr(), _stream_handle(stream, x))
     check("mgs_quant_rows128", st)
@@ -189,12 +178,13 @@ def mgs_quant_blocks128(w: torch.Tensor, pow2: bool = False, transposed: bool = 
     _need(w, "w", _BF16_LIKE, 3)
     E, N, K = w.shape
     nb, kb = (N + 127) // 128, (K + 127) // 128
-    q = torch.empty((E, N, K), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((E, nb, kb), dtype=torch.float32, device=w.device)
+    empty = _allocator(stream, w.device)
+    q = empty((E, N, K), dtype=torch.uint8, device=w.device)
+    scales = empty((E, nb, kb), dtype=torch.float32, device=w.device)
     q_t = scales_t = None
     if transposed:
-        q_t = torch.empty((E, K, N), dtype=torch.uint8, device=w.device)
-        scales_t = torch.empty((E, kb, nb), dtype=torch.float32, device=w.device)
+        q_t = empty((E, K, N), dtype=torch.uint8, device=w.device)
+        scales_t = empty((E, kb, nb), dtype=torch.float32, device=w.device)
     st = lib().mgs_quant_blocks128(w.data_ptr(), E, N, K, MGS_FLAG_POW2_SCALE if pow2 else 0, q.data_ptr(),
                                    scales.data_ptr(), _ptr(q_t), _ptr(scales_t), _stream_handle(stream, w))
     check("mgs_quant_blocks128", st)
@@ -226,7 +216,7 @@ def mgs_mm_block128(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_
     if offsets is not None:
         _input(offsets, a, "offsets", (torch.int32,), (E,))
     kind = _out_type(out_dtype)
-    y = _out(y, (M, N), out_dtype, a.device, "y")
+    y = _out(y, (M, N), out_dtype, a.device, "y", stream)
     st = lib().mgs_mm_block128(a.data_ptr(), a_scales.data_ptr(), M, K, b.data_ptr(), b_scales.data_ptr(), E, N,
                                _ptr(offsets), MGS_FLAG_FAST_ACCUM if fast_accum else 0, kind, y.data_ptr(),
                                _stream_handle(stream, a))
@@ -255,7 +245,7 @@ def mgs_mm_wgrad(a_t: torch.Tensor, a_scales_t: torch.Tensor, b_t: torch.Tensor,
     kind = _out_type(out_dtype)
     if accumulate and dw is None:
         raise MgsError("mgs_mm_wgrad", MGS_ERR_INVALID_ARG, ": accumulate needs dw")
-    dw = _out(dw, (G, N, K), out_dtype, a_t.device, "dw")
+    dw = _out(dw, (G, N, K), out_dtype, a_t.device, "dw", stream)
     flags = (MGS_FLAG_ACCUMULATE if accumulate else 0) | (MGS_FLAG_FAST_ACCUM if fast_accum else 0)
     st = lib().mgs_mm_wgrad(a_t.data_ptr(), a_scales_t.data_ptr(), b_t.data_ptr(), b_scales_t.data_ptr(), M, N, K,
                             offsets.data_ptr(), G, flags, kind, dw.data_ptr(),

@@ -38,13 +38,16 @@ __global__ __launch_bounds__(256) void rows128_kernel(const uint16_t* __restrict
 // column at a time: both orders cost one read of w. Streaming stores: the
 // outputs are larger than the caches. 16 x 8192 x 5120, 2.68 GB with both orders:
 // 530 us back to back, 5.1 TB/s (plain stores of q: 557).
-__global__ __launch_bounds__(256) void blocks128_kernel(const uint16_t* __restrict__ w, int64_t N, int64_t K,
-                                                        int pow2, uint8_t* __restrict__ q, float* __restrict__ scales,
-                                                        uint8_t* __restrict__ q_t, float* __restrict__ scales_t) {
+__global__ __launch_bounds__(256) void blocks128_kernel(const uint16_t* __restrict__ w, int64_t E, int64_t N,
+                                                        int64_t K, int pow2, uint8_t* __restrict__ q,
+                                                        float* __restrict__ scales, uint8_t* __restrict__ q_t,
+                                                        float* __restrict__ scales_t) {
     __shared__ uint32_t s_max[4];
     __shared__ uint32_t s_t[128][32 + 1];
     const int64_t nbk = (K + 127) / 128, nbn = (N + 127) / 128;
-    const int64_t bk = blockIdx.x % nbk, rest = blockIdx.x / nbk, bn = rest % nbn, e = rest / nbn;
+    const uint32_t block = (uint32_t)workgroup_xz();        // the host has checked that 31 bits hold E nbn nbk
+    const int64_t bk = block % nbk, rest = block / nbk, bn = rest % nbn, e = rest / nbn;
+    if (e >= E) return;
     const int cv = threadIdx.x & 15, rq = threadIdx.x / 16;
     const int64_t col = bk * 128 + cv * 8, row0 = bn * 128;
     auto row_of = [&](int j) { return row0 + rq * 4 + (j & 3) + (j >> 2) * 64; };
@@ -110,8 +113,8 @@ hipError_t launch_rows128(const uint16_t* x, int64_t M, int64_t K, bool pow2, ui
 hipError_t launch_blocks128(const uint16_t* w, int64_t E, int64_t N, int64_t K, bool pow2, uint8_t* q,
                             float* scales, uint8_t* q_t, float* scales_t, hipStream_t stream) {
     const int64_t blocks = E * ((N + 127) / 128) * ((K + 127) / 128);
-    hipLaunchKernelGGL(blocks128_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, w, N, K, pow2 ? 1 : 0, q,
-                       scales, q_t, scales_t);
+    hipLaunchKernelGGL(blocks128_kernel, grid_xz(blocks), dim3(256), 0, stream, w, E, N, K, pow2 ? 1 : 0, q, scales,
+                       q_t, scales_t);
     return hipGetLastError();
 }
 

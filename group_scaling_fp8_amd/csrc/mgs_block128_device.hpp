@@ -6,6 +6,16 @@
 
 namespace mgs {
 
+// A launch has fewer than 2^32 threads along x (with more, the count wraps and
+// the rest of the grid does not run): more workgroups go on along z. The last
+// run along x may pass the end.
+__device__ __forceinline__ int64_t workgroup_xz() { return blockIdx.x + (int64_t)gridDim.x * blockIdx.z; }
+inline dim3 grid_xz(int64_t blocks, unsigned y = 1) {
+    constexpr int64_t kMaxX = 1 << 22;       // of at most 512 threads
+    const int64_t x = blocks < kMaxX ? blocks : kMaxX;
+    return dim3((unsigned)x, y, (unsigned)((blocks + x - 1) / x));
+}
+
 // Max over the 16 lanes of a DPP row, in every lane of it (rotations by 8, 4,
 // 2 and 1): with 8 columns a lane, the maximum of a block of 128.
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {

@@ -324,14 +324,6 @@ __global__ __launch_bounds__(kFusedThreads) void dispatch_fused_kernel(DispatchA
 // columns, 0.84 GB: 154 us, 5.5 TB/s.
 constexpr int kZeroRows = 16;
 
-// A launch has at most 2^32 threads along x: more workgroups go on along z.
-__device__ __forceinline__ int64_t workgroup_xz() { return blockIdx.x + (int64_t)gridDim.x * blockIdx.z; }
-dim3 grid_xz(int64_t blocks, unsigned y) {
-    constexpr int64_t kMaxX = 1 << 23;
-    const int64_t x = blocks < kMaxX ? blocks : kMaxX;
-    return dim3((unsigned)x, y, (unsigned)((blocks + x - 1) / x));
-}
-
 template <int U>
 __global__ __launch_bounds__(kDispatchThreads) void dispatch_kernel(DispatchArgs a, int tokens) {
     __shared__ int s_row[kWave];

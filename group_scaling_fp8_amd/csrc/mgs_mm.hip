@@ -795,9 +795,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     };
     int g = -1, begin, end;                // the group and its rows, wgrad: its part of the contraction
     int m0, n0;
+    const int64_t wg = workgroup_xz();     // may pass the last tile
     if constexpr (WGRAD) {
         const int row_tiles = (int)((p.N + BM - 1) / BM), per = row_tiles * col_tiles;
-        const int L = tile_of(blockIdx.x, p.G * per);
+        if (wg >= p.G * per) return;
+        const int L = tile_of((int)wg, p.G * per);
         g = uniform(L / per);
         for (int base = 0; base <= g; base += kWave) {
             group(base + lane, carry);
@@ -815,8 +817,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
             carry = uniform(__shfl(e, kWave - 1, kWave));
         }
         const int last_end = carry, total = (tiles + (M - last_end + BM - 1) / BM) * col_tiles;
-        if ((int)blockIdx.x >= total) return;
-        const int L = tile_of(blockIdx.x, total);
+        if (wg >= total) return;
+        const int L = tile_of((int)wg, total);
         int before = tiles;
         begin = last_end;
         end = M;
@@ -953,9 +955,9 @@ hipError_t launch_few(const MmArgs& p, bool f32, hipStream_t stream) {
     const int64_t blocks = down * ((p.cols + kFewCols - 1) / kFewCols);
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
     if (f32)
-        hipLaunchKernelGGL((mm_few_kernel<BM, WGRAD, true>), dim3((unsigned)blocks), dim3(kFewWaves * 64), 0, stream, p);
+        hipLaunchKernelGGL((mm_few_kernel<BM, WGRAD, true>), grid_xz(blocks), dim3(kFewWaves * 64), 0, stream, p);
     else
-        hipLaunchKernelGGL((mm_few_kernel<BM, WGRAD, false>), dim3((unsigned)blocks), dim3(kFewWaves * 64), 0, stream, p);
+        hipLaunchKernelGGL((mm_few_kernel<BM, WGRAD, false>), grid_xz(blocks), dim3(kFewWaves * 64), 0, stream, p);
     return hipGetLastError();
 }
 

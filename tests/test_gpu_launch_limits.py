@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import experts_ref as ref
 import group_scaling_fp8_amd as mgs
 from gpu_util import dev, to_dev
 
@@ -46,6 +47,24 @@ def test_weight_cast_of_more_than_2_to_the_24_matrices():
     # amax is a whole number from 1 to 8 (256 values: never 0 here), so s holds one of eight values
     values = torch.full((8,), 448.0, device="cuda") / torch.arange(1, 9, device="cuda")
     assert bool(torch.isin(s.view(-1), values).all())
+
+
+def test_few_rows_of_more_tiles_than_2_to_the_23():
+    """A workgroup of 512 threads for each: more than 2^32 threads."""
+    G, M, N, K = 1024, 20480, 120000, 16
+    rng = np.random.default_rng(2)
+    a = rng.integers(0x30, 0x48, (M, K)).astype(np.uint8)
+    b = torch.randint(0x30, 0x48, (G, N, K), generator=generator(2), device="cuda", dtype=torch.uint8)
+    sa = np.exp2(rng.integers(-3, 4, (M, 1))).astype(np.float32)
+    sb = np.exp2(rng.integers(-3, 4, (G, -(-N // 128), 1))).astype(np.float32)
+    ends = np.arange(20, M + 1, 20).astype(np.int32)
+    y = mgs.mgs_mm_block128(to_dev(a), to_dev(sa), b, to_dev(sb), to_dev(ends))
+    for first in (0, 59904, N - 64):      # starts of blocks of 128 columns
+        cols = slice(first, min(first + 128, N))
+        part = np.ascontiguousarray(sb[:, first // 128:first // 128 + 1])
+        want, mag = ref.mm_block128(a, sa, b[:, cols].cpu().numpy(), part, ends)
+        err = np.abs(y[:, cols].double().cpu().numpy() - want)
+        assert (err <= ref.mm_tolerance(want, mag, K, "bf16")).all(), first
 
 
 def test_combine_of_wide_rows():

@@ -297,16 +297,17 @@ __global__ __launch_bounds__(kFusedThreads) void dispatch_fused_kernel(DispatchA
 
     // rows without a slot: place r of every group, dealt out over all waves
     const int waves = gridDim.x * kFusedWaves, w = blockIdx.x * kFusedWaves + wave;
-    const int places = E * a.align, tail = (int)(a.P - s_start[E]);
-    for (int base = w; base < places + tail; base += waves * kWave) {
-        const int i = base + lane * waves;
+    const int places = E * a.align;
+    const int64_t all = places + a.P - s_start[E];       // P may be near 2^31: 64 bits
+    for (int64_t base = w; base < all; base += waves * kWave) {
+        const int64_t i = base + lane * waves;
         int p = -1;
         if (i < places) {
-            const int e = i / a.align;
-            p = s_start[e] + s_total[e] + i - e * a.align;
+            const int e = (int)i / a.align;
+            p = s_start[e] + s_total[e] + (int)i - e * a.align;
             if (p >= s_start[e + 1]) p = -1;
-        } else if (i < places + tail) {
-            p = s_start[E] + i - places;
+        } else if (i < all) {
+            p = (int)(s_start[E] + i - places);
         }
         for (uint64_t left = __ballot(p >= 0); left; left &= left - 1) {
             const int row = __shfl(p, __builtin_ctzll(left), kWave);

@@ -89,3 +89,22 @@ def test_dispatch_of_wide_rows():
     want_q, want_s = mgs.mgs_quant_rows128(x)
     assert torch.equal(xp[:1], x) and torch.equal(q[:1], want_q) and torch.equal(s[:1], want_s)
     assert not bool(xp[1:].any()) and not bool(q[1:].any())
+
+
+@pytest.mark.parametrize("T", [3, 40000])
+def test_order_into_nearly_2_to_the_31_rows(T):
+    """The C call with as many rows as it takes, by one launch and ranked: every
+    row past the groups is marked as empty."""
+    k, E, align, P = 1, 1024, 4096, (1 << 31) - 1
+    rng = np.random.default_rng(T)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    ids_d, slots = to_dev(ids), torch.zeros((P,), dtype=torch.int32, device="cuda")
+    off, rows = torch.empty((E,), dtype=torch.int32, device="cuda"), torch.empty((T, k), dtype=torch.int32, device="cuda")
+    ws = torch.empty((256 * E,), dtype=torch.uint8, device="cuda")
+    st = mgs.lib().mgs_moe_dispatch(None, T, 0, ids_d.data_ptr(), k, E, align, 0, P, off.data_ptr(), rows.data_ptr(),
+                                    slots.data_ptr(), None, None, None, ws.data_ptr(), ws.numel(), None)
+    assert st == mgs.MGS_OK
+    r_off, r_rows, r_slots = ref.order(ids, E, align)
+    assert np.array_equal(off.cpu().numpy(), r_off) and np.array_equal(rows.cpu().numpy(), r_rows)
+    assert np.array_equal(slots[:len(r_slots)].cpu().numpy(), r_slots)
+    assert all(bool((part == -1).all()) for part in slots[len(r_slots):].split(1 << 28))

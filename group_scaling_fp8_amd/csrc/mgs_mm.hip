@@ -24,6 +24,7 @@
 #include "mgs_block128_device.hpp"
 #include "mgs_experts.hpp"
 #include "mgs_kernels.hpp"
+#include "mgs_mm_form.hpp"
 
 namespace mgs {
 
@@ -761,7 +762,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
 // while this one is multiplied; sums are exact (the matrix cores have nothing else
 // to do). The waves' sums meet in LDS and are added in wave order. Bound by the
 // loads: one row by 8192 x 8192 17 us, 4 TB/s.
-constexpr int kFewCols = 32, kFewWaves = 8;
+constexpr int kFewWaves = 8;
 
 // The 32 bytes at p + at of a row of len bytes (a multiple of 16, not 0), zeros
 // past its end.
@@ -979,56 +980,15 @@ hipError_t launch(const MmArgs& p, bool f32, int cus, hipStream_t stream) {
     return hipGetLastError();
 }
 
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Which form a product takes, from the sizes the host knows (us, MI355X):
-// - few rows: up to 20 rows a group on average, one row of fragments (M = 1 by
-//   8192 x 8192: 17, against 66 on tiles of 128 x 128; more rows a group only
-//   where there is one group: 512 rows in 16 groups by 2048 x 4096 take 58, and
-//   33 on tiles); up to 40 rows two, and four where that is at most one
-//   workgroup a CU (64 rows by 8192 x 8192: 39 and 66; 256 rows by 4096 x 4096,
-//   two a CU: 36 and 32).
-// - few outputs of wgrad: the same form with the fewest rows a tile that still
-//   leaves one workgroup a CU (16640 x 256 x 272: 25 with 16 rows, 48 with 64, and
-//   66 on tiles of 128 x 128 in two parts; 16384 x 1024 x 512: 48 and 60, twice as
-//   many outputs 93 and 61; with binary32 sums still 93 and 94, and 43 and 52 in
-//   four groups of 512 x 512).
-// - 256 x 256 tiles where they fill the CUs, twice if groups end inside them
-//   (block128 16640 x 5120 x 8192 in 16 groups: 780, and about 1000 with 128 x
-//   128; 2048 x 4096 x 4096, half the CUs: 66 and 48) and, for wgrad, where the
-//   contraction is long or the tiles are many (16640 x 8192 x 5120 in 16 groups:
-//   745, and about 950; 4096 x 2048 x 2048 in 8 groups, four steps a tile: 40 and
-//   32).
-// - 128 x 128 tiles otherwise, two workgroups a CU (block128 with binary32 sums
-//   has no registers for more: 256 x 128 took 1591, 128 x 128 1491; 128 x 64,
-//   three a CU, did not gain on 1003 x 4176 x 4112, and lost a third on
-//   8192 x 8192 x 4096); where they leave half the CUs idle, two sets of waves
-//   share a tile's contraction (256 x 4096 x 4096: 27 to 22; wgrad 8192 x 1024 x
-//   1024 in two groups: 44 to 37; with binary32 sums block128 does not gain).
 template <bool WGRAD, bool FAST>
 hipError_t launch_sized(const MmArgs& p, bool f32, int cus, hipStream_t stream) {
-    const int64_t groups = p.offsets ? p.G : 1;
-    if constexpr (WGRAD) {
-        const int64_t across = groups * up(p.K, kFewCols);
-        if (across * up(p.N, 16) <= cus) return launch_few<16, true>(p, f32, stream);
-        if (across * up(p.N, 32) <= cus) return launch_few<32, true>(p, f32, stream);
-        if (across * up(p.N, 64) <= (FAST ? cus : 2 * cus)) return launch_few<64, true>(p, f32, stream);
-        const int64_t tiles = groups * up(p.N, 256) * up(p.K, 256);
-        if (tiles >= cus && (p.M / groups >= 2048 || tiles >= 4 * cus))
-            return launch<256, 256, 128, 64, 1, true, FAST>(p, f32, cus, stream);
-    } else {
-        const int64_t rows = up(p.M, groups);
-        if (rows <= 20) return launch_few<16, false>(p, f32, stream);
-        if (groups == 1 && rows <= 40) return launch_few<32, false>(p, f32, stream);
-        if (groups == 1 && up(p.M, 64) * up(p.N, kFewCols) <= cus) return launch_few<64, false>(p, f32, stream);
-        if constexpr (FAST) {
-            if ((up(p.M, 256) + groups / 2) * up(p.N, 256) >= (groups == 1 ? cus : 2 * cus))
-                return launch<256, 256, 128, 64, 1, false, true>(p, f32, cus, stream);
-        }
-    }
+    const MmForm form = mm_form(WGRAD, FAST, p.offsets != nullptr, p.M, p.N, p.K, p.G, cus);
+    if (form.few == 16) return launch_few<16, WGRAD>(p, f32, stream);
+    if (form.few == 32) return launch_few<32, WGRAD>(p, f32, stream);
+    if (form.few == 64) return launch_few<64, WGRAD>(p, f32, stream);
     if constexpr (WGRAD || FAST) {
-        const int64_t tiles = (WGRAD ? groups * up(p.N, 128) : p.M / 128 + (p.offsets ? p.G + 1 : 1)) * up(p.cols, 128);
-        if (2 * tiles <= cus) return launch<128, 128, 64, 64, 2, WGRAD, FAST>(p, f32, cus, stream);
+        if (form.tile == 256) return launch<256, 256, 128, 64, 1, WGRAD, FAST>(p, f32, cus, stream);
+        if (form.sets == 2) return launch<128, 128, 64, 64, 2, WGRAD, FAST>(p, f32, cus, stream);
     }
     return launch<128, 128, 64, 64, 1, WGRAD, FAST>(p, f32, cus, stream);
 }

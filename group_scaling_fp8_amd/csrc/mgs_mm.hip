@@ -678,7 +678,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
 #pragma unroll
             for (int j = 0; j < NT; ++j) acc[i][j] += sums[(i * NT + j) * (WAVES * 64)];
     }
-    if (t.len == 0) {        // whatever the scales of no rows are
+    const bool empty = t.len == 0;
+    if (empty) {             // whatever the scales of no rows are: here, and where wgrad scales below
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -707,13 +708,13 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
             ib[j] = *reinterpret_cast<const v4f*>(
                 scale + BM + wn + (F32 ? j * 16 + fg * 4 : (j >> 1) * 32 + fg * 8 + (j & 1) * 4));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ib[j][c] = 1.0f / ib[j][c];
+            for (int c = 0; c < 4; ++c) ib[j][c] = empty ? 0.0f : 1.0f / ib[j][c];
         }
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         if constexpr (WGRAD) {
-            const float ia = 1.0f / scale[wm + fr + i * 16];
+            const float ia = empty ? 0.0f : 1.0f / scale[wm + fr + i * 16];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll

@@ -282,20 +282,29 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(const uint4* __restrict_
 
 }  // namespace
 
+// A launch has fewer than 2^32 threads (with more, the count wraps and the
+// rest of the grid does not run): longer arrays take several, of this many
+// workgroups.
+constexpr int64_t kMaxBlocks = 1 << 23;
+static_assert(kMaxBlocks * kThreads < (int64_t(1) << 32), "threads of a launch");
+
 hipError_t launch_mx(const uint16_t* x, int64_t n_elems, bool rceil, uint8_t* q, uint8_t* scales,
                      hipStream_t stream) {
-    const int64_t n_vec = n_elems / 8;
-    const int64_t per_block = (int64_t)kThreads * kMxVecs;
-    const int64_t blocks = (n_vec + per_block - 1) / per_block;
-    hipLaunchKernelGGL(mx_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, x, n_vec,
-                       rceil ? 1 : 0, q, scales);
-    return hipGetLastError();
+    const int64_t per_block = (int64_t)kThreads * kMxVecs * 8, run = kMaxBlocks * per_block;
+    for (int64_t at = 0; at < n_elems; at += run) {
+        const int64_t n = n_elems - at < run ? n_elems - at : run, blocks = (n + per_block - 1) / per_block;
+        hipLaunchKernelGGL(mx_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, x + at, n / 8,
+                           rceil ? 1 : 0, q + at, scales + at / 32);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_mx_dim1(const uint16_t* x, int64_t M, int64_t K, bool rceil, uint8_t* q_t,
                           uint8_t* scales_t, hipStream_t stream) {
     const int64_t tiles = ((M + kMxRows - 1) / kMxRows) * ((K + kMxCols - 1) / kMxCols);
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    if (tiles * kMxThreads >= int64_t(1) << 32) return hipErrorInvalidValue;
     hipLaunchKernelGGL(mx_dim1_kernel, dim3((unsigned)tiles), dim3(kMxThreads), 0, stream, x, M, K,
                        rceil ? 1 : 0, q_t, scales_t);
     return hipGetLastError();
@@ -312,11 +321,15 @@ hipError_t launch_mx_dequant(const uint8_t* q, const uint8_t* scales, int64_t n_
 }
 
 hipError_t launch_cast(const float* in, int64_t n, uint8_t* out, hipStream_t stream) {
-    const int64_t n4 = n / 4;
-    const int64_t blocks = (n4 + kThreads - 1) / kThreads;
-    hipLaunchKernelGGL(cast_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream,
-                       reinterpret_cast<const float4*>(in), n4, reinterpret_cast<uint32_t*>(out));
-    return hipGetLastError();
+    const int64_t per_block = (int64_t)kThreads * 4, run = kMaxBlocks * per_block;
+    for (int64_t at = 0; at < n; at += run) {
+        const int64_t m = n - at < run ? n - at : run, blocks = (m + per_block - 1) / per_block;
+        hipLaunchKernelGGL(cast_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream,
+                           reinterpret_cast<const float4*>(in + at), m / 4, reinterpret_cast<uint32_t*>(out + at));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_copy(const void* src, void* dst, int64_t bytes, hipStream_t stream) {

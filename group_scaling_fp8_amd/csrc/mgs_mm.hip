@@ -15,8 +15,9 @@
 //          rate. It aligns the products of each eight consecutive k to the
 //          largest of the eight and drops what lies below 2^-13 of it (measured
 //          bit by bit on the card); the sums of the eights are binary32. The
-//          loss is about 5e-5 of a typical sum, a thirtieth of a bf16 output's
-//          own rounding.
+//          loss is at most 2^-10 of the sum of the terms' magnitudes (where one
+//          of eight is far larger than the rest) and about 5e-5 of a typical
+//          sum, a thirtieth of a bf16 output's own rounding.
 //
 // An instruction's K order is free as long as both operands use the same one,
 // so a lane holds the 16-byte chunks g and g + 4 (g = lane / 16) of its row's
@@ -128,8 +129,11 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // out of eight, the row's bits 0, 1 and 3.
 
 // A wave's share of the loads of one step's rows of 128 bytes into LDS, 16 bytes
-// a lane straight from memory. Rows past the valid ones repeat the last one
-// (their products are never stored); bytes outside the contraction are zero.
+// a lane straight from memory. Rows past the tile's last one are whatever follows
+// in the array (the next group's rows, the next expert's weight: perhaps not
+// numbers) and zeros past its end; a sum holds one row of A and one of B, and the
+// output descriptor's size drops those of the surplus rows. Bytes outside the
+// contraction are zero.
 struct Loads {
     v4i src;
     uint32_t voff, step, lds;        // of the lane's first row, to the next load's, of the wave's first line
@@ -294,21 +298,28 @@ __device__ __forceinline__ void wait_some_or_none(int some) {
 // out to as many sets of waves, each with buffers of its own; their sums are
 // added in LDS at the end.
 //
-// What bounds it, by form (rates of dense products, MI355X; the library's plain
-// E4M3 product reaches 2600 TFLOP/s at 8192^3, its bf16 product 1400):
-//   256 x 256 fast    block128 2150 TFLOP/s, wgrad 2780 (16384 x 8192 x 8192). A
-//                     step's 32 matrix instructions a wave, two waves a SIMD,
-//                     take 2048 cycles; block128 adds 128 fmas a wave for the
-//                     scaled sums, which stand in the gaps between them, and the
-//                     eight waves read 192 KiB of LDS in about 1500 cycles beside
-//                     the 512 that the loads write.
-//   exact             block128 1080 TFLOP/s, wgrad 1580: the bf16 instructions
+// What bounds it, by form (rates of dense products of 16384 x 8192 x 8192, MI355X;
+// the library's plain products reach 3240 TFLOP/s in E4M3 and 1600 in bf16 at
+// 16384^3, with the matrix cores busy 91% of the time):
+//   256 x 256 fast    block128 2190 TFLOP/s, wgrad 2910. A step's 32 matrix
+//                     instructions a wave, two waves a SIMD, take 2048 cycles;
+//                     block128 adds 128 fmas a wave for the scaled sums, which
+//                     stand in the gaps between them, and the eight waves read
+//                     192 KiB of LDS in about 1500 cycles beside the 512 that the
+//                     loads write. In a layer of ragged groups (32768 rows, 8192 x
+//                     5120) the matrix cores are busy 49% of the time.
+//   exact             block128 1110 TFLOP/s, wgrad 1590: the bf16 instructions
 //                     take twice the cycles, and every wave widens the bytes of
 //                     its fragments itself, which takes issue slots.
-//                     (Under these loads the card lowers its clock to 2.0 GHz, and
-//                     to 1.7 where the matrix cores are busy nine cycles in ten.)
-//   few tiles         latency: two steps' loads (64 KiB a CU) are in flight, and a
-//                     CU takes in 35 to 45 KB/us whatever the form.
+//   outputs           a tile's stores drain under one step of the next tile: from
+//                     its second step on, each wait is for all that came before.
+//                     Short contractions (eight steps a tile: wgrad of 16640 rows
+//                     in 16 groups) pay for output and sums one after the other.
+//   few tiles         latency: two steps' loads (64 KiB a CU) are in flight. 128 x
+//                     128 tiles of 4096 rows in 16 groups by 4096 x 4096 take in 39
+//                     KB/us a CU, with the matrix cores busy 26% of the time.
+// (The clock falls as the matrix cores are used more: 1.9 to 2.0 GHz in the large
+// products here, 1.5 to 1.6 under the library's.)
 template <int BM, int BN, int WM, int WN, int PARTS, bool WGRAD, bool FAST, bool F32>
 __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel(MmArgs p) {
     constexpr int WAVES = BM / WM * (BN / WN);             // of one part

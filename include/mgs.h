@@ -444,7 +444,8 @@ int mgs_mm_block128(const void *a, const float *a_scales, int64_t M, int64_t K, 
  *                    not read as values.
  *   flags            MGS_FLAG_ACCUMULATE to add to what dw holds,
  *                    MGS_FLAG_FAST_ACCUM.
- *   dw               (n_groups, N, K), written; an empty group gives zeros.
+ *   dw               (n_groups, N, K), written; an empty group gives zeros,
+ *                    whatever its scales are.
  * Requirements: M, N and K multiples of 16, M < 2^23 - 256, K < 2^21 - 64,
  * n_groups <= MGS_MAX_GROUPS; a_t, b_t and dw 16-byte aligned.
  */

@@ -7,7 +7,10 @@ token's results are summed with its router weights:
 
 Weights are cast once per step in blocks of 128 x 128, in both orders; rows are
 cast in blocks of 128; the weight gradients read the transposed per-group casts
-(mgs_quant_groups_dim0_t), which keep one scale for each column and group.
+(mgs_quant_groups_dim0_t), which keep one scale for each column and group. The
+products with bf16 results ask for the faster sums (fast_accum), whose loss is at
+most 2^-10 of the sum of a result's terms in magnitude and mostly far below the
+rounding to bf16; the weight gradients are summed in binary32.
 
     python examples/experts_layer.py --tokens 4096 --hidden 4096 --inner 2048 --experts 16 --top-k 2
 """

@@ -279,6 +279,8 @@ int mgs_mx_quant_dim0(const void *x, int64_t M, int64_t K,
  *             of rows 32 * (r / 32) .. + 31 of column k.
  *   scales_t  (K, M/32) bytes, E8M0 (exponent + 127).
  * Requirements: x and q_t 16-byte aligned. M == 0 or K == 0 is a no-op.
+ * Errors: MGS_ERR_HIP if ceil(M / 512) * ceil(K / 128) reaches 2^22, more
+ * than one launch holds.
  */
 int mgs_mx_quant_dim1(const void *x, int64_t M, int64_t K, int mode,
                       void *q_t, uint8_t *scales_t, void *stream);

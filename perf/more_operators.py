@@ -295,21 +295,23 @@ def _plain_product(st):
 
 def _own_run(st):
     import group_scaling_fp8_amd as mgs
+    from group_scaling_fp8_amd import feedforward
     case, op = st["case"], st["case"]["op"]
     if op == "cast":
-        q, s = mgs.mgs_quant_rows_i8(st["x"])
+        q, s = feedforward.mgs_quant_rows_i8(st["x"])
         return {"q": q, "scales": s}
     args = (st["a"], st["a_scales"], st["b"], st["b_scales"])
     if op == "product":
-        return {"y": mgs.mgs_mm_i8(*args, st["offsets"], torch.float32 if case["f32"] else torch.bfloat16)}
+        return {"y": feedforward.mgs_mm_i8(*args, st["offsets"], torch.float32 if case["f32"] else torch.bfloat16)}
     act = mgs.MGS_ACT_SILU if case["act"] == "silu" else mgs.MGS_ACT_GELU
     if op == "gated8":
-        return {"h": mgs.mgs_mm_gated_i8(*args, st["offsets"], act)}
+        return {"h": feedforward.mgs_mm_gated_i8(*args, st["offsets"], act)}
     if op == "gated":
-        out = mgs.mgs_mm_gated_block128(*args, st["offsets"], act, fast_accum=case["fast"], keep=case["keep"])
+        out = feedforward.mgs_mm_gated_block128(*args, st["offsets"], act, fast_accum=case["fast"],
+                                                keep=case["keep"])
         return {"h": out[0], "gu": out[1]} if case["keep"] else {"h": out}
-    out = mgs.mgs_mm_gated_grad_block128(*args, st["gu"], st["offsets"], act, fast_accum=case["fast"],
-                                         hidden=case["hidden"])
+    out = feedforward.mgs_mm_gated_grad_block128(*args, st["gu"], st["offsets"], act, fast_accum=case["fast"],
+                                                 hidden=case["hidden"])
     return {"dgu": out[0], "h": out[1]} if case["hidden"] else {"dgu": out}
 
 

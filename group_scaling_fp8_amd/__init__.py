@@ -4,13 +4,14 @@ The functions below carry the names of the C entry points in include/mgs.h
 and only marshal arguments: they check torch tensors, allocate outputs the
 caller did not pass, and call the library on the current HIP stream. Every
 step of the computation runs in the library's HIP kernels. There is no CPU
-fallback: if libmgs.so is missing, the first call raises.
+fallback: if libmgs.so is missing, the first call raises. The calls of gated
+feed-forward layers and of 8-bit integers are in the module ``feedforward``.
 """
 from __future__ import annotations
 
 from ._lib import (  # noqa: F401
-    MGS_ERR_HIP, MGS_ERR_INVALID_ARG, MGS_ERR_UNSUPPORTED, MGS_FLAG_ACCUMULATE, MGS_FLAG_FAST_ACCUM,
-    MGS_FLAG_POW2_SCALE, MGS_FLAG_VALIDATE, MGS_MAX_GROUPS, MGS_MOE_MAX_TOP_K,
+    MGS_ACT_GELU, MGS_ACT_SILU, MGS_ERR_HIP, MGS_ERR_INVALID_ARG, MGS_ERR_UNSUPPORTED, MGS_FLAG_ACCUMULATE,
+    MGS_FLAG_FAST_ACCUM, MGS_FLAG_POW2_SCALE, MGS_FLAG_VALIDATE, MGS_I8_MAX_K, MGS_MAX_GROUPS, MGS_MOE_MAX_TOP_K,
     MGS_MX_FLOOR, MGS_MX_RCEIL, MGS_OK, MGS_OUT_BF16, MGS_OUT_F32, MgsError, lib, library_path,
 )
 from .api import (  # noqa: F401
@@ -22,3 +23,4 @@ from .experts import (  # noqa: F401
     mgs_mm_block128, mgs_mm_wgrad, mgs_moe_combine, mgs_moe_combine_grad, mgs_moe_dispatch, mgs_moe_rows,
     mgs_moe_sort, mgs_quant_blocks128, mgs_quant_rows128,
 )
+from . import feedforward  # noqa: E402,F401  (the gated feed-forward and 8-bit integer calls)

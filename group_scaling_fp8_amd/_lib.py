@@ -24,6 +24,9 @@ MGS_FLAG_FAST_ACCUM = 8
 MGS_OUT_BF16 = 0
 MGS_OUT_F32 = 1
 MGS_MOE_MAX_TOP_K = 64
+MGS_ACT_SILU = 0
+MGS_ACT_GELU = 1
+MGS_I8_MAX_K = 131056
 
 EXPORTS = (
     "mgs_quant_groups_dim0", "mgs_dim0_workspace_bytes", "mgs_quant_groups_dim0_ws",
@@ -33,6 +36,7 @@ EXPORTS = (
     "mgs_mx_quant_dim1", "mgs_mx_dequant_dim0", "mgs_cast_e4m3",
     "mgs_copy", "mgs_moe_rows", "mgs_moe_workspace_bytes", "mgs_moe_dispatch", "mgs_moe_combine",
     "mgs_moe_combine_grad", "mgs_quant_rows128", "mgs_quant_blocks128", "mgs_mm_block128", "mgs_mm_wgrad",
+    "mgs_mm_gated_block128", "mgs_mm_gated_grad_block128", "mgs_quant_rows_i8", "mgs_mm_i8", "mgs_mm_gated_i8",
     "mgs_test_quant_dim0", "mgs_status_string", "mgs_last_hip_error",
 )
 
@@ -98,7 +102,14 @@ def lib():
                             ("mgs_quant_rows128", [vp, i64, i64, u32, vp, vp, vp]),
                             ("mgs_quant_blocks128", [vp, i64, i64, i64, u32, vp, vp, vp, vp, vp]),
                             ("mgs_mm_block128", [vp, vp, i64, i64, vp, vp, i32, i64, vp, u32, ctypes.c_int, vp, vp]),
-                            ("mgs_mm_wgrad", [vp, vp, vp, vp, i64, i64, i64, vp, i32, u32, ctypes.c_int, vp, vp])):
+                            ("mgs_mm_wgrad", [vp, vp, vp, vp, i64, i64, i64, vp, i32, u32, ctypes.c_int, vp, vp]),
+                            ("mgs_mm_gated_block128", [vp, vp, i64, i64, vp, vp, i32, i64, vp, ctypes.c_int, u32, vp, vp,
+                                                       vp]),
+                            ("mgs_mm_gated_grad_block128", [vp, vp, i64, i64, vp, vp, i32, i64, vp, ctypes.c_int, u32,
+                                                            vp, vp, vp, vp]),
+                            ("mgs_quant_rows_i8", [vp, i64, i64, vp, vp, vp]),
+                            ("mgs_mm_i8", [vp, vp, i64, i64, vp, vp, i32, i64, vp, ctypes.c_int, vp, vp]),
+                            ("mgs_mm_gated_i8", [vp, vp, i64, i64, vp, vp, i32, i64, vp, ctypes.c_int, vp, vp])):
             fn = getattr(L, name)
             fn.argtypes = types
             fn.restype = ctypes.c_int

@@ -75,4 +75,28 @@ hipError_t launch_mm_wgrad(const uint8_t* a_t, const float* a_scales_t, const ui
                            const float* b_scales_t, int64_t M, int64_t N, int64_t K, const int32_t* offsets,
                            int64_t G, bool fast, bool f32, bool accumulate, void* dw, int cus, hipStream_t stream);
 
+// ---- gated feed-forward layers (mgs_gated.hip) ---------------------------------------
+
+// b (2 E, F, K): matrices 2 e and 2 e + 1 are expert e's projections. gu null: only h.
+hipError_t launch_mm_gated(const uint8_t* a, const float* a_scales, int64_t M, int64_t K, const uint8_t* b,
+                           const float* b_scales, int64_t E, int64_t F, const int32_t* offsets, int act, bool fast,
+                           void* h, void* gu, int cus, hipStream_t stream);
+
+// D > 0. h null: only dgu.
+hipError_t launch_mm_gated_grad(const uint8_t* dy, const float* dy_scales, int64_t M, int64_t D, const uint8_t* b,
+                                const float* b_scales, int64_t E, int64_t F, const int32_t* offsets, int act,
+                                bool fast, const uint16_t* gu, void* dgu, void* h, int cus, hipStream_t stream);
+
+// ---- 8-bit integers (mgs_i8.hip) -------------------------------------------------------
+
+hipError_t launch_rows_i8(const uint16_t* x, int64_t M, int64_t K, uint8_t* q, float* scales, hipStream_t stream);
+
+hipError_t launch_mm_i8(const uint8_t* a, const float* a_scales, int64_t M, int64_t K, const uint8_t* b,
+                        const float* b_scales, int64_t E, int64_t N, const int32_t* offsets, bool f32, void* y,
+                        int cus, hipStream_t stream);
+
+hipError_t launch_mm_gated_i8(const uint8_t* a, const float* a_scales, int64_t M, int64_t K, const uint8_t* b,
+                              const float* b_scales, int64_t E, int64_t F, const int32_t* offsets, int act, void* h,
+                              int cus, hipStream_t stream);
+
 }  // namespace mgs

@@ -1,4 +1,4 @@
-// mgs_experts_api.hip — the C ABI of the mixture-of-experts calls (declared in
+// mgs_experts_api.hip — the C ABI of the calls of a layer of experts (declared in
 // include/mgs.h): host-side argument checks and stream-ordered launches.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -23,6 +23,29 @@ int check_order(int64_t T, int32_t top_k, int32_t n_experts, int32_t align) {
     if (T > INT32_MAX / 2 / top_k) return MGS_ERR_UNSUPPORTED;      // slots and rows are int32
     return MGS_OK;
 }
+
+// What every product of rows with each group's weight asks of its operands:
+// sizes, then pointers. MGS_OK with *done: there is nothing to compute.
+int check_rows(int64_t M, int64_t N, int64_t K, int32_t n_groups, const int32_t* offsets, int64_t max_k, bool* done) {
+    *done = false;
+    if (M < 0 || N < 0 || K < 0 || n_groups < 1 || N % 16 != 0 || K % 16 != 0) return MGS_ERR_INVALID_ARG;
+    if (!offsets && n_groups != 1) return MGS_ERR_INVALID_ARG;
+    if (n_groups > MGS_MAX_GROUPS || M > INT32_MAX || N > kMaxCols || K > max_k) return MGS_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) {
+        *done = true;
+        return MGS_OK;
+    }
+    if (!aligned(offsets, 4)) return MGS_ERR_INVALID_ARG;
+    if ((M / 16 + n_groups + 1) * ((N + 15) / 16) > INT32_MAX) return MGS_ERR_UNSUPPORTED;
+    return MGS_OK;
+}
+
+bool operands(const void* a, const float* a_scales, const void* b, const float* b_scales) {
+    return a && a_scales && b && b_scales && aligned(a, 16) && aligned(b, 16) && aligned(a_scales, 4) &&
+           aligned(b_scales, 4);
+}
+
+bool known(int act) { return act == MGS_ACT_SILU || act == MGS_ACT_GELU; }
 
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
@@ -170,6 +193,73 @@ int mgs_mm_wgrad(const void* a_t, const float* a_scales_t, const void* b_t, cons
                                            (flags & MGS_FLAG_FAST_ACCUM) != 0, out_type == MGS_OUT_F32,
                                            (flags & MGS_FLAG_ACCUMULATE) != 0, dw, mgs::device_cus(),
                                            as_stream(stream)));
+}
+
+int mgs_mm_gated_block128(const void* a, const float* a_scales, int64_t M, int64_t K, const void* b,
+                          const float* b_scales, int32_t n_groups, int64_t F, const int32_t* offsets, int act,
+                          uint32_t flags, void* h, void* gu, void* stream) {
+    if (!known(act) || (flags & ~MGS_FLAG_FAST_ACCUM)) return MGS_ERR_INVALID_ARG;
+    bool done;
+    const int st = check_rows(M, F, K, n_groups, offsets, kMaxRowBytes, &done);
+    if (st != MGS_OK || done) return st;
+    if (!h || !aligned(h, 16) || !aligned(gu, 16)) return MGS_ERR_INVALID_ARG;
+    if (K > 0 && !operands(a, a_scales, b, b_scales)) return MGS_ERR_INVALID_ARG;
+    return hip_status(mgs::launch_mm_gated(static_cast<const uint8_t*>(a), a_scales, M, K,
+                                           static_cast<const uint8_t*>(b), b_scales, n_groups, F, offsets, act,
+                                           (flags & MGS_FLAG_FAST_ACCUM) != 0, h, gu, mgs::device_cus(),
+                                           as_stream(stream)));
+}
+
+int mgs_mm_gated_grad_block128(const void* dy, const float* dy_scales, int64_t M, int64_t D, const void* b,
+                               const float* b_scales, int32_t n_groups, int64_t F, const int32_t* offsets, int act,
+                               uint32_t flags, const void* gu, void* dgu, void* h, void* stream) {
+    if (!known(act) || (flags & ~MGS_FLAG_FAST_ACCUM)) return MGS_ERR_INVALID_ARG;
+    bool done;
+    const int st = check_rows(M, F, D, n_groups, offsets, kMaxRowBytes, &done);
+    if (st != MGS_OK || done) return st;
+    if (D == 0) return MGS_ERR_INVALID_ARG;
+    if (!gu || !dgu || !aligned(gu, 16) || !aligned(dgu, 16) || !aligned(h, 16)) return MGS_ERR_INVALID_ARG;
+    if (!operands(dy, dy_scales, b, b_scales)) return MGS_ERR_INVALID_ARG;
+    return hip_status(mgs::launch_mm_gated_grad(static_cast<const uint8_t*>(dy), dy_scales, M, D,
+                                                static_cast<const uint8_t*>(b), b_scales, n_groups, F, offsets, act,
+                                                (flags & MGS_FLAG_FAST_ACCUM) != 0,
+                                                static_cast<const uint16_t*>(gu), dgu, h, mgs::device_cus(),
+                                                as_stream(stream)));
+}
+
+int mgs_quant_rows_i8(const void* x, int64_t M, int64_t K, void* q, float* scales, void* stream) {
+    if (M < 0 || K < 0 || K % 8 != 0) return MGS_ERR_INVALID_ARG;
+    if (K > INT32_MAX || M > INT32_MAX) return MGS_ERR_UNSUPPORTED;
+    if (M == 0 || K == 0) return MGS_OK;
+    if (!x || !q || !scales || !aligned(x, 16) || !aligned(q, 8) || !aligned(scales, 4)) return MGS_ERR_INVALID_ARG;
+    return hip_status(mgs::launch_rows_i8(static_cast<const uint16_t*>(x), M, K, static_cast<uint8_t*>(q), scales,
+                                          as_stream(stream)));
+}
+
+int mgs_mm_i8(const void* a, const float* a_scales, int64_t M, int64_t K, const void* b, const float* b_scales,
+              int32_t n_groups, int64_t N, const int32_t* offsets, int out_type, void* y, void* stream) {
+    if (out_type != MGS_OUT_BF16 && out_type != MGS_OUT_F32) return MGS_ERR_INVALID_ARG;
+    bool done;
+    const int st = check_rows(M, N, K, n_groups, offsets, MGS_I8_MAX_K, &done);
+    if (st != MGS_OK || done) return st;
+    if (!y || !aligned(y, 16)) return MGS_ERR_INVALID_ARG;
+    if (K > 0 && !operands(a, a_scales, b, b_scales)) return MGS_ERR_INVALID_ARG;
+    return hip_status(mgs::launch_mm_i8(static_cast<const uint8_t*>(a), a_scales, M, K,
+                                        static_cast<const uint8_t*>(b), b_scales, n_groups, N, offsets,
+                                        out_type == MGS_OUT_F32, y, mgs::device_cus(), as_stream(stream)));
+}
+
+int mgs_mm_gated_i8(const void* a, const float* a_scales, int64_t M, int64_t K, const void* b, const float* b_scales,
+                    int32_t n_groups, int64_t F, const int32_t* offsets, int act, void* h, void* stream) {
+    if (!known(act)) return MGS_ERR_INVALID_ARG;
+    bool done;
+    const int st = check_rows(M, F, K, n_groups, offsets, MGS_I8_MAX_K, &done);
+    if (st != MGS_OK || done) return st;
+    if (!h || !aligned(h, 16)) return MGS_ERR_INVALID_ARG;
+    if (K > 0 && !operands(a, a_scales, b, b_scales)) return MGS_ERR_INVALID_ARG;
+    return hip_status(mgs::launch_mm_gated_i8(static_cast<const uint8_t*>(a), a_scales, M, K,
+                                              static_cast<const uint8_t*>(b), b_scales, n_groups, F, offsets, act, h,
+                                              mgs::device_cus(), as_stream(stream)));
 }
 
 }  // extern "C"

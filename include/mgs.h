@@ -455,6 +455,107 @@ int mgs_mm_wgrad(const void *a_t, const float *a_scales_t, const void *b_t, cons
                  int64_t N, int64_t K, const int32_t *offsets, int32_t n_groups, uint32_t flags, int out_type,
                  void *dw, void *stream);
 
+/* ---- gated feed-forward layers ----------------------------------------------
+ *
+ * An expert of a gated layer is (act(x Wg^T) * (x Wu^T)) Wd^T. One call
+ * computes both projections, the activation and the product; another, from the
+ * output's gradient, the gradients of both projections. The other products of
+ * the layer are mgs_mm_block128's and mgs_mm_wgrad's: the input gradient
+ * contracts the 2 F columns of dgu with the transposed cast of the weight as
+ * (n_groups, 2 F, K).
+ *
+ * act(g) = g * sigmoid(t(g)): MGS_ACT_SILU t = g, MGS_ACT_GELU the form with a
+ * hyperbolic tangent, t = 2 sqrt(2 / pi) (g + 0.044715 g^3).
+ */
+enum { MGS_ACT_SILU = 0, MGS_ACT_GELU = 1 };
+
+/*
+ * For m in group e, with fp32 sums as mgs_mm_block128 forms them:
+ *   g[m, n] = row m times row n of matrix 2 e,  u[m, n] = of matrix 2 e + 1
+ *   h[m, n] = act(g) * u, in fp32 from the sums, rounded once
+ *   a, a_scales  (M, K) E4M3 bytes, (M, ceil(K / 128)) fp32.
+ *   b, b_scales  (2 n_groups, F, K) E4M3 bytes, (2 n_groups, ceil(F / 128),
+ *                ceil(K / 128)) fp32: mgs_quant_blocks128 of 2 n_groups
+ *                matrices. Where F % 128 == 0 its cast of (n_groups, 2 F, K)
+ *                has the same bytes and scales.
+ *   offsets, flags  as for mgs_mm_block128. Rows past the last end give zeros.
+ *   h            (M, F) bf16, written.
+ *   gu           (M, 2 F) bf16, written: g, then u of each row, rounded from
+ *                the sums, which mgs_mm_gated_grad_block128 reads; or NULL.
+ * Requirements: F % 16 == 0, K % 16 == 0, K < 2^23 - 256, F < 2^21 - 64,
+ * n_groups <= MGS_MAX_GROUPS; a, b, h and gu 16-byte aligned; outputs overlap
+ * neither each other nor an input. K == 0 gives zeros.
+ */
+int mgs_mm_gated_block128(const void *a, const float *a_scales, int64_t M, int64_t K, const void *b,
+                          const float *b_scales, int32_t n_groups, int64_t F, const int32_t *offsets, int act,
+                          uint32_t flags, void *h, void *gu, void *stream);
+
+/*
+ * The gradients of both projections from the output's, for m in group e:
+ *   dh[m, n] = row m of dy times row n of matrix e, with fp32 sums
+ *   dg = dh * u * act'(g),  du = dh * act(g), each rounded once
+ *   dy, dy_scales  (M, D) E4M3 bytes, (M, ceil(D / 128)) fp32: the cast of the
+ *                output's gradient.
+ *   b, b_scales  (n_groups, F, D) E4M3 bytes, (n_groups, ceil(F / 128),
+ *                ceil(D / 128)) fp32: the transposed cast of the down weight
+ *                (n_groups, D, F).
+ *   offsets, flags  as for mgs_mm_block128. Rows past the last end give zeros.
+ *   gu           (M, 2 F) bf16, what the forward call kept. Rows past the last
+ *                end are not read as values.
+ *   dgu          (M, 2 F) bf16, written: dg, then du of each row.
+ *   h            (M, F) bf16, written: act(g) * u again, for the down weight's
+ *                gradient, so that the forward's need not be kept; it is
+ *                computed from the rounded gu, so the two differ by their
+ *                rounding. Or NULL.
+ * Requirements: as above with D for K; gu and dgu 16-byte aligned; D > 0 unless
+ * M or F is 0.
+ */
+int mgs_mm_gated_grad_block128(const void *dy, const float *dy_scales, int64_t M, int64_t D, const void *b,
+                               const float *b_scales, int32_t n_groups, int64_t F, const int32_t *offsets, int act,
+                               uint32_t flags, const void *gu, void *dgu, void *h, void *stream);
+
+/* ---- 8-bit integers ---------------------------------------------------------
+ *
+ * Products of serving: activations and weights in 8-bit integers with one scale
+ * for each token and each output channel. Sums are exact (32-bit integers), so
+ * a result depends neither on other rows nor on how the call splits its work.
+ */
+
+/* The most columns of a contraction: 2^17 products of any two bytes would pass
+ * 32 bits. */
+#define MGS_I8_MAX_K 131056
+
+/*
+ * One scale for each row: x (M, K) bf16, scales (M) fp32 = fl32(127 /
+ * max(amax, 1e-12)), q (M, K) int8 = fl32(x * scale) rounded to the nearest
+ * integer, ties to even: -127 to 127. x is finite. The weights of E experts
+ * (E, N, K) are E * N rows. Requirements: K % 8 == 0; x 16-byte aligned, q
+ * 8-byte aligned. M == 0 or K == 0 is a no-op.
+ */
+int mgs_quant_rows_i8(const void *x, int64_t M, int64_t K, void *q, float *scales, void *stream);
+
+/*
+ * For m in group e: y[m, n] = sum_k a[m, k] * b[e, n, k] / (a_scales[m] *
+ * b_scales[e, n]); the sum is exact and rounded to fp32 before it is scaled.
+ *   a, a_scales  (M, K) int8, (M) fp32.
+ *   b, b_scales  (n_groups, N, K) int8, (n_groups, N) fp32.
+ *   offsets, out_type, y  as for mgs_mm_block128. Rows past the last end give
+ *                zeros.
+ * The scales are finite and positive. Requirements: N % 16 == 0, K % 16 == 0,
+ * K <= MGS_I8_MAX_K, N < 2^21 - 64, n_groups <= MGS_MAX_GROUPS; a, b and y
+ * 16-byte aligned. K == 0 gives zeros.
+ */
+int mgs_mm_i8(const void *a, const float *a_scales, int64_t M, int64_t K, const void *b, const float *b_scales,
+              int32_t n_groups, int64_t N, const int32_t *offsets, int out_type, void *y, void *stream);
+
+/*
+ * mgs_mm_gated_block128's h of 8-bit integers: g and u are mgs_mm_i8's fp32
+ * products with matrices 2 e and 2 e + 1 of b (2 n_groups, F, K), b_scales
+ * (2 n_groups, F); h (M, F) bf16. Requirements as for mgs_mm_i8 with F for N.
+ */
+int mgs_mm_gated_i8(const void *a, const float *a_scales, int64_t M, int64_t K, const void *b, const float *b_scales,
+                    int32_t n_groups, int64_t F, const int32_t *offsets, int act, void *h, void *stream);
+
 /*
  * TEST ONLY (not part of the product interface): the dim0-family cast with
  * two launch parameters overridden, so tests can reach paths that the

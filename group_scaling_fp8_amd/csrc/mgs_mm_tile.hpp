@@ -56,7 +56,9 @@ struct Kind {
     static constexpr bool eight = NUM != Num::Exact;                // the instruction reads the bytes themselves
     static constexpr bool scaled = !wgrad && NUM != Num::Int8;      // every block of 128 has scales of its own
     static constexpr bool f32 = F32, more = MORE;
-    using few = Kind<JOB, NUM == Num::Int8 ? Num::Int8 : Num::Exact, F32, MORE>;     // the form for few rows
+    // the form for few rows: with the matrix cores idle, block128 and wgrad sum exactly
+    using few = Kind<JOB, NUM == Num::Fast && !gated && !grad ? Num::Exact : NUM, F32, MORE>;
+    static constexpr bool halves = gated || grad || NUM == Num::Int8;    // which 16 bytes of a line a lane takes (few rows)
 };
 
 // One output tile: rows of operand A down, rows of operand B across.
@@ -108,8 +110,10 @@ __device__ __forceinline__ void load4_lds(v4i rsrc, uint32_t off, uint32_t lds) 
 #endif
 }
 
-// 16 bytes a lane to the descriptor's base + off, as output written once; with
-// `add`, added to the four binary32 values there.
+// 16 bytes a lane to the descriptor's base + off, as output written once or, in
+// halves of lines, through L2 (POLICY 0); with `add`, added to the four binary32
+// values there.
+template <int POLICY = kLoadNontemporal>
 __device__ __forceinline__ void store16(v4i rsrc, uint32_t off, v4i v, bool add) {
 #ifdef __HIP_DEVICE_COMPILE__
     typedef unsigned int v4u __attribute__((ext_vector_type(4)));
@@ -117,7 +121,7 @@ __device__ __forceinline__ void store16(v4i rsrc, uint32_t off, v4i v, bool add)
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, rsrc[2], rsrc[3]);
     if (add) v = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, v) +
                                              __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0)));
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, off, 0, kLoadNontemporal);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, off, 0, POLICY);
 #endif
 }
 
@@ -831,7 +835,9 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
         return v4i{(int)bf16x2(x[0], x[1]), (int)bf16x2(x[2], x[3]), (int)bf16x2(y[0], y[1]), (int)bf16x2(y[2], y[3])};
     };
     if constexpr (GATED) {
-        // a lane holds eight columns of both projections: 16 bytes of each output
+        // A lane holds eight columns of both projections: 16 bytes of each output. A
+        // wave's 32 columns are half a line, whose other half the next wave stores: L2
+        // joins them (16640 x 8192 x 5120 in 16 groups 1691 us, streaming stores 1758).
         const uint32_t pitch2 = pitch * 2;
         const int c = wn / 2 + fg * 8;
         const uint32_t inside = t.n0 + c < p.cols ? 0 : kOutOfRange;
@@ -847,14 +853,16 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) h[j][e] = p.act.of(r[j][e]) * r[j + 2][e];
-            store16(out, at + i * 16 * pitch, packed(h[0], h[1]), false);
+            store16<0>(out, at + i * 16 * pitch, packed(h[0], h[1]), false);
             if constexpr (MORE) {
-                store16(kept, at2 + i * 16 * pitch2, packed(r[0], r[1]), false);
-                store16(kept, at2 + i * 16 * pitch2 + pitch, packed(r[2], r[3]), false);
+                store16<0>(kept, at2 + i * 16 * pitch2, packed(r[0], r[1]), false);
+                store16<0>(kept, at2 + i * 16 * pitch2 + pitch, packed(r[2], r[3]), false);
             }
         }
     } else if constexpr (GRAD) {
-        // of each 32 columns a lane holds eight: 16 bytes of both projections and of each output
+        // 64 columns as they are stored below: the first piece of a lane is of rows
+        // 0-7 of sixteen, the second of rows 8-15, so that eight lanes load and
+        // store whole lines of both projections and of the outputs
         const uint32_t pitch2 = pitch * 2;
         const v4i gu = descriptor(reinterpret_cast<const uint8_t*>(p.gu), t.m0 * (int64_t)pitch2 + t.n0 * 2,
                                   p.M * (int64_t)pitch2);
@@ -864,46 +872,55 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
         if constexpr (MORE)
             hidden = descriptor(static_cast<uint8_t*>(p.more), t.m0 * (int64_t)pitch + t.n0 * 2,
                                 t.row_end * (int64_t)pitch);
-        uint32_t at[2], at2[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int c = wn + q * 32 + fg * 8;
-            const uint32_t inside = t.n0 + c < p.cols ? 0 : kOutOfRange;
-            at[q] = (wm + fr) * pitch + c * 2 + inside;
-            at2[q] = (wm + fr) * pitch2 + c * 2 + inside;
-        }
-        v4i g[2], u[2];
+        const int c = wn + (fg + (fr >> 3) * 4) * 8;
+        const uint32_t inside = t.n0 + c < p.cols ? 0 : kOutOfRange;
+        const uint32_t at = (wm + (fr & 7)) * pitch + c * 2 + inside, at2 = (wm + (fr & 7)) * pitch2 + c * 2 + inside;
+        v4i g[MT][2], u[MT][2];
+        // rows down an output, made where they are used: the compiler would keep every row's offset in registers
+        auto down = [](int rows, uint32_t pitch) {
+#ifdef __HIP_DEVICE_COMPILE__
+            asm volatile("" : "+s"(pitch));
+#endif
+            return rows * pitch;
+        };
         auto fetch = [&](int i) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                g[q] = load16(gu, at2[q] + i * 16 * pitch2);
-                u[q] = load16(gu, at2[q] + i * 16 * pitch2 + pitch);
+                const uint32_t off = at2 + down(i * 16 + q * 8, pitch2);
+                g[i][q] = load16(gu, off);
+                u[i][q] = load16(gu, off + pitch);
             }
+            __builtin_amdgcn_sched_barrier(0);
         };
         fetch(0);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             v4f r[NT];
             scaled_row(i, r);
-            v4i gi[2] = {g[0], g[1]}, ui[2] = {u[0], u[1]};
-            if (i + 1 < MT) fetch(i + 1);        // while this row is worked on
+            float dh[2][8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int first = __float_as_int(r[e >> 2][e & 3]), second = __float_as_int(r[2 + (e >> 2)][e & 3]);
+                dh[0][e] = __int_as_float(__builtin_amdgcn_update_dpp(first, second, 0x128, 0xF, 0xC, false));
+                dh[1][e] = __int_as_float(__builtin_amdgcn_update_dpp(second, first, 0x128, 0xF, 0x3, false));
+            }
+            if (i + 1 < MT) fetch(i + 1);        // more rows ahead spill: two 1059 us, three 1196, one 1010
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 v4i dg, du, h;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const v4f dh = r[2 * q + (e >> 1)];
-                    const int e2 = (e & 1) * 2;
-                    const GatedGrad lo = p.act.grad(dh[e2], bf16_lo(gi[q][e]), bf16_lo(ui[q][e]));
-                    const GatedGrad hi = p.act.grad(dh[e2 + 1], bf16_hi(gi[q][e]), bf16_hi(ui[q][e]));
+                    const GatedGrad lo = p.act.grad(dh[q][2 * e], bf16_lo(g[i][q][e]), bf16_lo(u[i][q][e]));
+                    const GatedGrad hi = p.act.grad(dh[q][2 * e + 1], bf16_hi(g[i][q][e]), bf16_hi(u[i][q][e]));
                     dg[e] = (int)bf16x2(lo.dg, hi.dg);
                     du[e] = (int)bf16x2(lo.du, hi.du);
                     h[e] = (int)bf16x2(lo.h, hi.h);
                 }
                 const v4i zero = {};             // rows of no group, whatever their projections are
-                store16(both, at2[q] + i * 16 * pitch2, empty ? zero : dg, false);
-                store16(both, at2[q] + i * 16 * pitch2 + pitch, empty ? zero : du, false);
-                if constexpr (MORE) store16(hidden, at[q] + i * 16 * pitch, empty ? zero : h, false);
+                const uint32_t off = at2 + down(i * 16 + q * 8, pitch2);
+                store16(both, off, empty ? zero : dg, false);
+                store16(both, off + pitch, empty ? zero : du, false);
+                if constexpr (MORE) store16(hidden, at + down(i * 16 + q * 8, pitch), empty ? zero : h, false);
             }
         }
     } else {
@@ -961,12 +978,13 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
 // loads: one row by 8192 x 8192 17 us, 4 TB/s.
 constexpr int kFewWaves = 8;
 
-// The 32 bytes at p + at of a row of len bytes (a multiple of 16, not 0), zeros
-// past its end.
+// The 16 bytes at p + at and those at APART bytes from them, of a row of len bytes
+// (a multiple of 16, not 0); zeros past its end.
+template <int APART>
 __device__ __forceinline__ v8i load32(const uint8_t* p, int64_t at, int64_t len) {
-    const bool first = at < len, second = at + 16 < len;
+    const bool first = at < len, second = at + APART < len;
     const v4i lo = *reinterpret_cast<const v4i*>(p + (first ? at : 0));
-    const v4i hi = *reinterpret_cast<const v4i*>(p + (second ? at + 16 : 0));
+    const v4i hi = *reinterpret_cast<const v4i*>(p + (second ? at + APART : 0));
     const v4i zero = {};
     return __builtin_shufflevector(first ? lo : zero, second ? hi : zero, 0, 1, 2, 3, 4, 5, 6, 7);
 }
@@ -985,146 +1003,174 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     const int64_t nnb = (p.N + 127) / 128;
     const int col_tiles = (int)((p.cols + COLS - 1) / COLS), M = (int)p.M;
 
-    // ---- which tile: every wave finds it, 64 groups at a time ----
+    // ---- the tiles: every wave finds them, 64 groups at a time ----
     constexpr int kAlign = WGRAD ? 16 : 1;
-    int carry = 0, tiles = 0;
-    int e = 0, b = 0;                      // this lane's group
-    auto group = [&](int g, int from) {
+    int e = 0, b = 0, upto = 0;            // of this lane's group: its rows, and the row tiles up to its end
+    auto group = [&](int g, int from, int before) {
         int raw = 0;
         if (g < p.G) raw = p.offsets ? min(max(p.offsets[g], 0), M) / kAlign * kAlign : M;
         e = max(wave_prefix_imax(raw), from);
         b = __shfl_up(e, 1, kWave);
         if (lane == 0) b = from;
-        return wave_prefix_sum((e - b + BM - 1) / BM);
+        upto = before + wave_prefix_sum((e - b + BM - 1) / BM);
     };
-    int g = -1, begin, end;                // the group and its rows, wgrad: its part of the contraction
-    int m0, n0;
-    const int64_t wg = workgroup_xz();     // may pass the last tile
+    const int row_tiles = (int)((p.N + BM - 1) / BM);                  // wgrad: down one matrix
+    int last_end = 0, tiles = 0, total;
     if constexpr (WGRAD) {
-        const int row_tiles = (int)((p.N + BM - 1) / BM), per = row_tiles * col_tiles;
-        if (wg >= p.G * per) return;
-        const int L = tile_of((int)wg, p.G * per);
-        g = uniform(L / per);
-        for (int base = 0; base <= g; base += kWave) {
-            group(base + lane, carry);
-            carry = uniform(__shfl(e, kWave - 1, kWave));
-        }
-        begin = uniform(__shfl(b, g % kWave, kWave));
-        end = uniform(__shfl(e, g % kWave, kWave));
-        m0 = uniform(L - g * per) % row_tiles * BM;
-        n0 = uniform(L - g * per) / row_tiles * COLS;
+        total = p.G * row_tiles * col_tiles;
     } else {
-        int upto = 0;
         for (int base = 0; base < p.G; base += kWave) {
-            upto = tiles + group(base + lane, carry);
+            group(base + lane, last_end, tiles);
             tiles = uniform(__shfl(upto, kWave - 1, kWave));
-            carry = uniform(__shfl(e, kWave - 1, kWave));
+            last_end = uniform(__shfl(e, kWave - 1, kWave));
         }
-        const int last_end = carry, total = (tiles + (M - last_end + BM - 1) / BM) * col_tiles;
-        if (wg >= total) return;
-        const int L = tile_of((int)wg, total);
+        total = (tiles + (M - last_end + BM - 1) / BM) * col_tiles;    // the rows past the last group give zeros
+    }
+    struct FewTile {
+        int g, begin, end;                 // the group (-1: none) and its rows, wgrad: its part of the contraction
+        int m0, n0;
+    };
+    auto locate = [&](int w) {
+        const int L = tile_of(w, total);
+        FewTile t;
+        if constexpr (WGRAD) {
+            const int per = row_tiles * col_tiles;
+            t.g = uniform(L / per);
+            int carry = 0;
+            for (int base = 0; base <= t.g; base += kWave) {
+                group(base + lane, carry, 0);
+                carry = uniform(__shfl(e, kWave - 1, kWave));
+            }
+            t.begin = uniform(__shfl(b, t.g % kWave, kWave));
+            t.end = uniform(__shfl(e, t.g % kWave, kWave));
+            t.m0 = uniform(L - t.g * per) % row_tiles * BM;
+            t.n0 = uniform(L - t.g * per) / row_tiles * COLS;
+            return t;
+        }
         int before = tiles;
-        begin = last_end;
-        end = M;
+        t.g = -1;
+        t.begin = last_end;
+        t.end = M;
         if (L < tiles * col_tiles) {
+            int base = 0;
             if (p.G > kWave) {
-                carry = tiles = 0;
-                for (int base = 0;; base += kWave) {
-                    upto = tiles + group(base + lane, carry);
-                    g = base;
-                    const int now = uniform(__shfl(upto, kWave - 1, kWave));
-                    if (L < now * col_tiles) break;
-                    tiles = now;
+                for (int carry = 0, passed = 0;; base += kWave) {
+                    group(base + lane, carry, passed);
+                    passed = uniform(__shfl(upto, kWave - 1, kWave));
+                    if (L < passed * col_tiles) break;
                     carry = uniform(__shfl(e, kWave - 1, kWave));
                 }
-            } else {
-                g = 0;
             }
             const int at = __builtin_ctzll(__ballot(upto * col_tiles > L));
-            g = uniform(g + at);
-            begin = uniform(__shfl(b, at, kWave));
-            end = uniform(__shfl(e, at, kWave));
-            before = uniform(__shfl(upto, at, kWave)) - (end - begin + BM - 1) / BM;
+            t.g = uniform(base + at);
+            t.begin = uniform(__shfl(b, at, kWave));
+            t.end = uniform(__shfl(e, at, kWave));
+            before = uniform(__shfl(upto, at, kWave)) - (t.end - t.begin + BM - 1) / BM;
         }
-        const int rows = (end - begin + BM - 1) / BM, local = L - before * col_tiles;
-        m0 = begin + local % rows * BM;
-        n0 = local / rows * COLS;
-    }
-    const int64_t row_end = WGRAD ? p.N : end;
-    const int64_t stride = WGRAD ? p.M : p.K, len = WGRAD ? end - begin : p.K;
-    const int nkb = (int)((len + kBK - 1) / kBK);
+        const int rows = (t.end - t.begin + BM - 1) / BM, local = L - before * col_tiles;
+        t.m0 = t.begin + local % rows * BM;
+        t.n0 = local / rows * COLS;
+        return t;
+    };
+    const int64_t grid = (int64_t)gridDim.x * gridDim.z;
+    int64_t wg = workgroup_xz();           // may pass the last tile
+    if (wg >= total) return;
 
     // ---- the contraction ----
     const int fr = lane & 15, fg = lane / 16;
-    Acc acc[MT][NT];
+    int64_t len;
+    int nkb;
+    const uint8_t *pa[MT], *pb[NT];
+    const float *psa[MT], *psb[BLOCKS];
+    // A block of the contraction: its bytes and scales, in registers from their loads to their products.
+    struct Block {
+        v8i a[MT], b[NT];
+        float sa[MT], sb[BLOCKS];
+    };
+    auto fetch = [&](Block& x, int k) {
+        const int64_t at = (int64_t)k * kBK + fg * (KIND::halves ? 16 : 32);
+        auto get = [&](const uint8_t* q) { return load32<KIND::halves ? 64 : 16>(q, at, len); };
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = Acc{0, 0, 0, 0};
-    if (g >= 0 && len > 0) {
-        const uint8_t *pa[MT], *pb[NT];
-        const float *psa[MT], *psb[BLOCKS];
-#pragma unroll
-        for (int w = 0; w < BLOCKS; ++w) psb[w] = p.b_scales + (((int64_t)g * BLOCKS + w) * nnb + n0 / 128) * nkb;
+        for (int j = 0; j < NT; ++j) x.b[j] = get(pb[j]);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const int64_t r = min((int64_t)m0 + i * 16 + fr, row_end - 1);
-            pa[i] = p.a + r * stride + (WGRAD ? begin : 0);
+            x.a[i] = get(pa[i]);
+            if constexpr (SCALED) x.sa[i] = psa[i][k];
+        }
+        if constexpr (SCALED)
+#pragma unroll
+            for (int w = 0; w < BLOCKS; ++w) x.sb[w] = psb[w][k];
+    };
+    Acc acc[MT][NT];
+    auto multiply = [&](const Block& x) {
+        float f[MT][BLOCKS];
+        if constexpr (SCALED)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int w = 0; w < BLOCKS; ++w) f[i][w] = (1.0f / x.sa[i]) * (1.0f / x.sb[w]);
+        Op ob[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) ob[j] = Op(x.b[j]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            if constexpr (!SCALED) {
+                Op::mfma(ob, Op(x.a[i]), acc[i]);
+            } else {
+                v4f part[NT] = {};
+                Op::mfma(ob, Op(x.a[i]), part);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[i][j][c] = fmaf(part[j][c], f[i][GATED ? j : 0], acc[i][j][c]);
+            }
+        }
+    };
+    Block x;
+    // Where t's operands are, and the loads of each wave's first blocks.
+    auto begin = [&](const FewTile& t) {
+        len = t.g < 0 ? 0 : WGRAD ? t.end - t.begin : p.K;
+        nkb = (int)((len + kBK - 1) / kBK);
+        if (len == 0) return;
+        const int64_t row_end = WGRAD ? p.N : t.end, stride = WGRAD ? p.M : p.K;
+#pragma unroll
+        for (int w = 0; w < BLOCKS; ++w) psb[w] = p.b_scales + (((int64_t)t.g * BLOCKS + w) * nnb + t.n0 / 128) * nkb;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int64_t r = min((int64_t)t.m0 + i * 16 + fr, row_end - 1);
+            pa[i] = p.a + r * stride + (WGRAD ? t.begin : 0);
             psa[i] = p.a_scales + r * nkb;
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int64_t r = min((int64_t)n0 + (GATED ? 0 : j * 16) + fr, p.cols - 1);
-            pb[j] = WGRAD ? p.b + r * stride + begin : p.b + (((int64_t)g * BLOCKS + (GATED ? j : 0)) * p.N + r) * stride;
+            const int64_t r = min((int64_t)t.n0 + (GATED ? 0 : j * 16) + fr, p.cols - 1);
+            pb[j] = WGRAD ? p.b + r * stride + t.begin
+                          : p.b + (((int64_t)t.g * BLOCKS + (GATED ? j : 0)) * p.N + r) * stride;
         }
-        v8i fa[MT], fb[NT];
-        float sa[MT], sb[BLOCKS];
-        auto fetch = [&](int k) {
-            const int64_t at = (int64_t)k * kBK + fg * 32;
-            auto get = [&](const uint8_t* q) { return load32(q, at, len); };
+        if (wave < nkb) fetch(x, wave);
+    };
+    FewTile t = locate((int)wg);
+    begin(t);
+    for (;;) {
+    const int64_t row_end = WGRAD ? p.N : t.end;
+    const int g = t.g, m0 = t.m0, n0 = t.n0;
+    const bool none = len == 0;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) fb[j] = get(pb[j]);
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                fa[i] = get(pa[i]);
-                if constexpr (SCALED) sa[i] = psa[i][k];
-            }
-            if constexpr (SCALED)
-#pragma unroll
-                for (int w = 0; w < BLOCKS; ++w) sb[w] = psb[w][k];
-        };
-        if (wave < nkb) fetch(wave);
-        for (int k = wave; k < nkb; k += kFewWaves) {
-            v8i na[MT], nb[NT];
-            float f[MT][BLOCKS];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) nb[j] = fb[j];
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                na[i] = fa[i];
-                if constexpr (SCALED)
-#pragma unroll
-                    for (int w = 0; w < BLOCKS; ++w) f[i][w] = (1.0f / sa[i]) * (1.0f / sb[w]);
-            }
-            if (k + kFewWaves < nkb) fetch(k + kFewWaves);
-            Op ob[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) ob[j] = Op(nb[j]);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                if constexpr (!SCALED) {
-                    Op::mfma(ob, Op(na[i]), acc[i]);
-                } else {
-                    v4f part[NT] = {};
-                    Op::mfma(ob, Op(na[i]), part);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            acc[i][j][c] = fmaf(part[j][c], f[i][GATED ? j : 0], acc[i][j][c]);
-                }
-            }
-        }
+        for (int j = 0; j < NT; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+    for (int k = wave; k < nkb; k += kFewWaves) {
+        const Block y = x;
+        if (k + kFewWaves < nkb) fetch(x, k + kFewWaves);
+        multiply(y);
+    }
+    // the next tile's first loads are on their way while this one is joined
+    wg += grid;
+    const bool more = wg < total;
+    if (more) {
+        t = locate((int)wg);
+        begin(t);
     }
 
     // ---- join and store ----
@@ -1144,7 +1190,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     // and the scales that are not in the sums yet, of output columns col to col + 3 of weight w
     auto scaled = [&](v4f v, int64_t row, int64_t col, int w) {
         if constexpr (WGRAD) {
-            if (len > 0) {
+            if (!none) {
                 const float ia = 1.0f / p.a_scales[row * p.G + g];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = v[i] * ia * (1.0f / p.b_scales[(col + i) * p.G + g]);
@@ -1202,16 +1248,21 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
             store4(p.out, (WGRAD ? g * p.N * p.cols : 0) + at, v);
         }
     }
+    if (!more) break;
+    __syncthreads();         // the sums are read before the next tile's are written
+    }
 }
 
 template <int BM, class KIND>
-hipError_t launch_few(const MmArgs& p, hipStream_t stream) {
+hipError_t launch_few(const MmArgs& p, int cus, hipStream_t stream) {
     constexpr bool WGRAD = KIND::wgrad;
     constexpr int COLS = KIND::gated ? kFewCols / 2 : kFewCols;
     const int64_t groups = p.offsets ? p.G + 1 : 1, spare = groups < p.M ? groups : p.M;
     const int64_t down = WGRAD ? p.G * ((p.N + BM - 1) / BM) : (p.M + spare * (BM - 1)) / BM;
-    const int64_t blocks = down * ((p.cols + COLS - 1) / COLS);
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t tiles = down * ((p.cols + COLS - 1) / COLS);
+    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t most = cus * (BM == 16 ? 16 : 8) / kFewWaves;
+    const int64_t blocks = WGRAD || tiles < most ? tiles : most;
     hipLaunchKernelGGL((mm_few_kernel<BM, KIND>), grid_xz(blocks), dim3(kFewWaves * 64), 0, stream, p);
     return hipGetLastError();
 }
@@ -1231,14 +1282,17 @@ hipError_t launch(const MmArgs& p, int cus, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The form by mm_form's rule; a gated pair of projections counts as one product
-// of twice the columns.
+// The form by the rules of mgs_mm_form.hpp; a gated pair of projections counts as one
+// product of twice the columns.
 template <class KIND>
 hipError_t launch_sized(const MmArgs& p, int cus, hipStream_t stream) {
-    const MmForm form = mm_form(KIND::wgrad, KIND::eight, p.offsets != nullptr, p.M, (KIND::gated ? 2 : 1) * p.N, p.K, p.G, cus);
-    if (form.few == 16) return launch_few<16, typename KIND::few>(p, stream);
-    if (form.few == 32) return launch_few<32, typename KIND::few>(p, stream);
-    if (form.few == 64) return launch_few<64, typename KIND::few>(p, stream);
+    const bool grouped = p.offsets != nullptr;
+    const MmForm form = KIND::halves
+                            ? mm_form_rows(KIND::eight, grouped, p.M, (KIND::gated ? 2 : 1) * p.N, p.G, cus)
+                            : mm_form(KIND::wgrad, KIND::eight, grouped, p.M, p.N, p.K, p.G, cus);
+    if (form.few == 16) return launch_few<16, typename KIND::few>(p, cus, stream);
+    if (form.few == 32) return launch_few<32, typename KIND::few>(p, cus, stream);
+    if (form.few == 64) return launch_few<64, typename KIND::few>(p, cus, stream);
     if constexpr (KIND::wgrad || KIND::eight) {
         if (form.tile == 256) return launch<256, 256, 128, 64, 1, KIND>(p, cus, stream);
         if (form.sets == 2) return launch<128, 128, 64, 64, 2, KIND>(p, cus, stream);

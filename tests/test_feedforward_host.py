@@ -1,8 +1,8 @@
 """CPU checks of the gated feed-forward and 8-bit integer calls: refusals of
 the C entry points before any GPU work, the Python front end, the form that
 each tested size takes, and the 64-bit forms that the GPU tests compare with."""
-import ctypes
 import inspect
+import subprocess
 
 import numpy as np
 import pytest
@@ -14,7 +14,7 @@ import group_scaling_fp8_amd as mgs
 from feedforward_cases import GATED, ROWS
 from group_scaling_fp8_amd import api, experts, feedforward
 from test_experts_host import A, INVALID, OK, UNSUPPORTED, with_defaults
-from test_mm_form import CUS, form  # noqa: F401  (a fixture)
+from test_mm_form import CSRC, CUS
 from test_output_streams import CURRENT, SIDE, Library, Stream, taken  # noqa: F401  (a fixture)
 
 CALLS = ("mgs_mm_gated_block128", "mgs_mm_gated_grad_block128", "mgs_quant_rows_i8", "mgs_mm_i8", "mgs_mm_gated_i8")
@@ -117,12 +117,51 @@ def test_memory_of_outputs(taken, monkeypatch, name, stream):  # noqa: F811
     assert [t.recorded for t in taken] == [[CURRENT] if stream else []] * outputs
 
 
+PROGRAM = r"""
+#include <stdio.h>
+#include "mgs_mm_form.hpp"
+int main() {
+    long long eight, grouped, M, N, G, cus;
+    while (scanf("%lld %lld %lld %lld %lld %lld", &eight, &grouped, &M, &N, &G, &cus) == 6) {
+        const mgs::MmForm f = mgs::mm_form_rows(eight, grouped, M, N, G, (int)cus);
+        printf("%d %d %d\n", f.few, f.tile, f.sets);
+    }
+    return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def form(tmp_path_factory):
+    d = tmp_path_factory.mktemp("rows")
+    (d / "form.cpp").write_text(PROGRAM)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", CSRC, "-o", str(d / "form"), str(d / "form.cpp")], check=True)
+
+    def run(*args):
+        r = subprocess.run([str(d / "form")], input=" ".join(str(int(a)) for a in args), capture_output=True, text=True,
+                           check=True)
+        return tuple(int(v) for v in r.stdout.split())
+    return run
+
+
 @pytest.mark.parametrize("gated,case", [(False, c) for c in ROWS] + [(True, c) for c in GATED])
-def test_sizes_take_their_forms(form, gated, case):  # noqa: F811
+def test_sizes_take_their_forms(form, gated, case):
+    """So that a changed rule cannot take a form out of the GPU tests unseen."""
     M, N, K, G, kind, eight, exact = case
     N *= 2 if gated else 1
-    assert form(0, 1, kind != "none", M, N, K, G, CUS) == eight
-    assert form(0, 0, kind != "none", M, N, K, G, CUS) == exact
+    assert form(1, kind != "none", M, N, G, CUS) == eight
+    assert form(0, kind != "none", M, N, G, CUS) == exact
+
+
+def test_limits_between_the_forms(form):
+    for args, want in (
+            ((1, 0, 1, 8192, 1), (16, 0, 0)), ((1, 0, 20, 16384, 1), (16, 0, 0)), ((1, 0, 21, 16384, 1), (32, 0, 0)),
+            ((1, 0, 41, 16384, 1), (0, 128, 2)), ((1, 1, 128, 16384, 16), (0, 128, 1)), ((0, 1, 128, 16384, 16), (16, 0, 0)),
+            ((1, 1, 32, 16384, 16), (16, 0, 0)), ((1, 0, 64, 4096, 1), (32, 0, 0)), ((1, 0, 128, 4096, 1), (64, 0, 0)),
+            ((1, 0, 256, 16384, 1), (0, 128, 2)), ((0, 0, 256, 16384, 1), (0, 128, 1)), ((1, 1, 256, 1040, 4), (64, 0, 0)),
+            ((1, 0, 2048, 4096, 1), (0, 128, 1)), ((1, 1, 2048, 4096, 8), (0, 256, 1)), ((1, 0, 1003, 4176, 1), (0, 128, 1)),
+            ((1, 1, 16640, 16384, 16), (0, 256, 1)), ((1, 0, 2147483647, 2097088, 1), (0, 256, 1))):
+        assert form(*args, CUS) == want, args
 
 
 # ---- the plain forms themselves -------------------------------------------------

@@ -30,7 +30,8 @@ int check_rows(int64_t M, int64_t N, int64_t K, int32_t n_groups, const int32_t*
     *done = false;
     if (M < 0 || N < 0 || K < 0 || n_groups < 1 || N % 16 != 0 || K % 16 != 0) return MGS_ERR_INVALID_ARG;
     if (!offsets && n_groups != 1) return MGS_ERR_INVALID_ARG;
-    if (n_groups > MGS_MAX_GROUPS || M > INT32_MAX || N > kMaxCols || K > max_k) return MGS_ERR_UNSUPPORTED;
+    // (rows are counted in 32 bits up to the end of their last tile)
+    if (n_groups > MGS_MAX_GROUPS || M >= INT32_MAX - 255 || N > kMaxCols || K > max_k) return MGS_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) {
         *done = true;
         return MGS_OK;

@@ -31,32 +31,47 @@ from ._lib import MGS_ACT_GELU, MGS_ACT_SILU, MGS_FLAG_FAST_ACCUM, check, lib
 from .api import _BF16_LIKE, _U8_LIKE, _need, _out, _stream_handle
 from .experts import _input, _out_type, _ptr
 
-_I8 = (torch.int8,)
+_I8, _F32, _I32 = (torch.int8,), (torch.float32,), (torch.int32,)
 
 
-def _operands(a, b, offsets, dtypes, matrices: int) -> Tuple[int, ...]:
-    """Checks rows a (M, K), weights b (matrices * E, N, K) and the E end offsets; M, K, E, N."""
+def _run(name: str, t: torch.Tensor, *args):
+    """Calls the entry point with t's device current: kernels are launched there."""
+    if t.get_device() == torch.cuda.current_device():
+        st = getattr(lib(), name)(*args)
+    else:
+        with torch.cuda.device(t.device):
+            st = getattr(lib(), name)(*args)
+    check(name, st)
+
+
+def _given(t, first, name: str, dtypes, shape):
+    """_input, with its checks in one expression: a call's host time counts where its kernel takes microseconds."""
+    if not (type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous() and
+            t.get_device() == first.get_device()):
+        _input(t, first, name, dtypes, shape)
+
+
+def _operands(a, a_scales, b, b_scales, offsets, dtypes, matrices: int) -> Tuple[int, ...]:
+    """Checks rows a (M, K) and weights b (matrices * E, N, K), their scales
+    (of blocks of 128, or of rows of 8-bit integers) and the E end offsets;
+    M, K, E, N."""
     _need(a, "a", dtypes, 2)
     M, K = a.shape
     _need(b, "b", dtypes, 3)
     W, N = b.shape[:2]
     if W % matrices:
         raise ValueError("b has %d matrices, %d for each group" % (W, matrices))
-    _input(b, a, "b", dtypes, (W, N, K))
+    _given(b, a, "b", dtypes, (W, N, K))
+    if dtypes is _I8:
+        _given(a_scales, a, "a_scales", _F32, (M,))
+        _given(b_scales, a, "b_scales", _F32, (W, N))
+    else:
+        kb = (K + 127) // 128
+        _given(a_scales, a, "a_scales", _F32, (M, kb))
+        _given(b_scales, a, "b_scales", _F32, (W, (N + 127) // 128, kb))
     if offsets is not None:
-        _input(offsets, a, "offsets", (torch.int32,), (W // matrices,))
+        _given(offsets, a, "offsets", _I32, (W // matrices,))
     return M, K, W // matrices, N
-
-
-def _block_scales(a, a_scales, b, b_scales):
-    kb = (a.shape[1] + 127) // 128
-    _input(a_scales, a, "a_scales", (torch.float32,), (a.shape[0], kb))
-    _input(b_scales, a, "b_scales", (torch.float32,), (b.shape[0], (b.shape[1] + 127) // 128, kb))
-
-
-def _row_scales(a, a_scales, b, b_scales):
-    _input(a_scales, a, "a_scales", (torch.float32,), (a.shape[0],))
-    _input(b_scales, a, "b_scales", (torch.float32,), tuple(b.shape[:2]))
 
 
 def _act(act: int) -> int:
@@ -75,16 +90,14 @@ def mgs_mm_gated_block128(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tens
     scales (2 E, ceil(F/128), ceil(K/128)). Returns h (M, F) bf16, act(g) * u,
     and with `keep` (or a passed gu) also gu (M, 2 F) bf16, g then u of each
     row. offsets and fast_accum are mgs_mm_block128's."""
-    M, K, E, F = _operands(a, b, offsets, _U8_LIKE, 2)
-    _block_scales(a, a_scales, b, b_scales)
+    M, K, E, F = _operands(a, a_scales, b, b_scales, offsets, _U8_LIKE, 2)
     act = _act(act)
     h = _out(h, (M, F), torch.bfloat16, a.device, "h", stream)
     if keep or gu is not None:
         gu = _out(gu, (M, 2 * F), torch.bfloat16, a.device, "gu", stream)
-    st = lib().mgs_mm_gated_block128(a.data_ptr(), a_scales.data_ptr(), M, K, b.data_ptr(), b_scales.data_ptr(), E, F,
-                                     _ptr(offsets), act, MGS_FLAG_FAST_ACCUM if fast_accum else 0, h.data_ptr(),
-                                     _ptr(gu), _stream_handle(stream, a))
-    check("mgs_mm_gated_block128", st)
+    _run("mgs_mm_gated_block128", a, a.data_ptr(), a_scales.data_ptr(), M, K, b.data_ptr(), b_scales.data_ptr(), E, F,
+         _ptr(offsets), act, MGS_FLAG_FAST_ACCUM if fast_accum else 0, h.data_ptr(),
+         _ptr(gu), _stream_handle(stream, a))
     return h if gu is None else (h, gu)
 
 
@@ -96,18 +109,16 @@ def mgs_mm_gated_grad_block128(dy: torch.Tensor, dy_scales: torch.Tensor, b: tor
     with scales (M, ceil(D/128)): b (E, F, D) and scales (E, ceil(F/128),
     ceil(D/128)) are the transposed cast of the down weight, gu (M, 2 F) bf16
     what the forward call kept. Returns dgu (M, 2 F) bf16, dg then du of each
-    row, and with `hidden` (or a passed h) also h (M, F) bf16, act(g) * u."""
-    M, D, E, F = _operands(dy, b, offsets, _U8_LIKE, 1)
-    _block_scales(dy, dy_scales, b, b_scales)
-    _input(gu, dy, "gu", _BF16_LIKE, (M, 2 * F))
+    row (a passed dgu may be gu), and with `hidden` (or a passed h) also h (M, F) bf16, act(g) * u."""
+    M, D, E, F = _operands(dy, dy_scales, b, b_scales, offsets, _U8_LIKE, 1)
+    _given(gu, dy, "gu", _BF16_LIKE, (M, 2 * F))
     act = _act(act)
     dgu = _out(dgu, (M, 2 * F), torch.bfloat16, dy.device, "dgu", stream)
     if hidden or h is not None:
         h = _out(h, (M, F), torch.bfloat16, dy.device, "h", stream)
-    st = lib().mgs_mm_gated_grad_block128(dy.data_ptr(), dy_scales.data_ptr(), M, D, b.data_ptr(), b_scales.data_ptr(),
-                                          E, F, _ptr(offsets), act, MGS_FLAG_FAST_ACCUM if fast_accum else 0,
-                                          gu.data_ptr(), dgu.data_ptr(), _ptr(h), _stream_handle(stream, dy))
-    check("mgs_mm_gated_grad_block128", st)
+    _run("mgs_mm_gated_grad_block128", dy, dy.data_ptr(), dy_scales.data_ptr(), M, D, b.data_ptr(), b_scales.data_ptr(),
+         E, F, _ptr(offsets), act, MGS_FLAG_FAST_ACCUM if fast_accum else 0,
+         gu.data_ptr(), dgu.data_ptr(), _ptr(h), _stream_handle(stream, dy))
     return dgu if h is None else (dgu, h)
 
 
@@ -121,9 +132,8 @@ def mgs_quant_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scales:
         raise ValueError("x must have 2 or 3 dims")
     q = _out(q, tuple(x.shape), torch.int8, x.device, "q", stream)
     scales = _out(scales, tuple(x.shape[:-1]), torch.float32, x.device, "scales", stream)
-    st = lib().mgs_quant_rows_i8(x.data_ptr(), scales.numel(), x.shape[-1], q.data_ptr(), scales.data_ptr(),
-                                 _stream_handle(stream, x))
-    check("mgs_quant_rows_i8", st)
+    _run("mgs_quant_rows_i8", x, x.data_ptr(), scales.numel(), x.shape[-1], q.data_ptr(), scales.data_ptr(),
+         _stream_handle(stream, x))
     return q, scales
 
 
@@ -134,13 +144,11 @@ def mgs_mm_i8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales
     (E, N, K) int8, scales (E, N), of the group that each row is in (int32 end
     offsets over M; None with E == 1: one dense product). Returns y (M, N);
     rows past the last group are zero. Sums are exact."""
-    M, K, E, N = _operands(a, b, offsets, _I8, 1)
-    _row_scales(a, a_scales, b, b_scales)
+    M, K, E, N = _operands(a, a_scales, b, b_scales, offsets, _I8, 1)
     kind = _out_type(out_dtype)
     y = _out(y, (M, N), out_dtype, a.device, "y", stream)
-    st = lib().mgs_mm_i8(a.data_ptr(), a_scales.data_ptr(), M, K, b.data_ptr(), b_scales.data_ptr(), E, N,
-                         _ptr(offsets), kind, y.data_ptr(), _stream_handle(stream, a))
-    check("mgs_mm_i8", st)
+    _run("mgs_mm_i8", a, a.data_ptr(), a_scales.data_ptr(), M, K, b.data_ptr(), b_scales.data_ptr(), E, N,
+         _ptr(offsets), kind, y.data_ptr(), _stream_handle(stream, a))
     return y
 
 
@@ -149,11 +157,9 @@ def mgs_mm_gated_i8(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_
                     stream=None) -> torch.Tensor:
     """mgs_mm_gated_block128's h (M, F) bf16 of 8-bit integers: a (M, K) int8
     with scales (M), b (2 E, F, K) int8 with scales (2 E, F)."""
-    M, K, E, F = _operands(a, b, offsets, _I8, 2)
-    _row_scales(a, a_scales, b, b_scales)
+    M, K, E, F = _operands(a, a_scales, b, b_scales, offsets, _I8, 2)
     act = _act(act)
     h = _out(h, (M, F), torch.bfloat16, a.device, "h", stream)
-    st = lib().mgs_mm_gated_i8(a.data_ptr(), a_scales.data_ptr(), M, K, b.data_ptr(), b_scales.data_ptr(), E, F,
-                               _ptr(offsets), act, h.data_ptr(), _stream_handle(stream, a))
-    check("mgs_mm_gated_i8", st)
+    _run("mgs_mm_gated_i8", a, a.data_ptr(), a_scales.data_ptr(), M, K, b.data_ptr(), b_scales.data_ptr(), E, F,
+         _ptr(offsets), act, h.data_ptr(), _stream_handle(stream, a))
     return h

@@ -482,9 +482,9 @@ enum { MGS_ACT_SILU = 0, MGS_ACT_GELU = 1 };
  *   h            (M, F) bf16, written.
  *   gu           (M, 2 F) bf16, written: g, then u of each row, rounded from
  *                the sums, which mgs_mm_gated_grad_block128 reads; or NULL.
- * Requirements: F % 16 == 0, K % 16 == 0, K < 2^23 - 256, F < 2^21 - 64,
- * n_groups <= MGS_MAX_GROUPS; a, b, h and gu 16-byte aligned; outputs overlap
- * neither each other nor an input. K == 0 gives zeros.
+ * Requirements: M < 2^31 - 256, F % 16 == 0, K % 16 == 0, K < 2^23 - 256,
+ * F < 2^21 - 64, n_groups <= MGS_MAX_GROUPS; a, b, h and gu 16-byte aligned;
+ * outputs overlap neither each other nor an input. K == 0 gives zeros.
  */
 int mgs_mm_gated_block128(const void *a, const float *a_scales, int64_t M, int64_t K, const void *b,
                           const float *b_scales, int32_t n_groups, int64_t F, const int32_t *offsets, int act,
@@ -502,13 +502,14 @@ int mgs_mm_gated_block128(const void *a, const float *a_scales, int64_t M, int64
  *   offsets, flags  as for mgs_mm_block128. Rows past the last end give zeros.
  *   gu           (M, 2 F) bf16, what the forward call kept. Rows past the last
  *                end are not read as values.
- *   dgu          (M, 2 F) bf16, written: dg, then du of each row.
+ *   dgu          (M, 2 F) bf16, written: dg, then du of each row. It may be gu
+ *                itself, whose values are read before they are overwritten.
  *   h            (M, F) bf16, written: act(g) * u again, for the down weight's
  *                gradient, so that the forward's need not be kept; it is
  *                computed from the rounded gu, so the two differ by their
  *                rounding. Or NULL.
- * Requirements: as above with D for K; gu and dgu 16-byte aligned; D > 0 unless
- * M or F is 0.
+ * The scales are finite and positive. Requirements: as above with D for K; gu and
+ * dgu 16-byte aligned; D > 0 unless M or F is 0.
  */
 int mgs_mm_gated_grad_block128(const void *dy, const float *dy_scales, int64_t M, int64_t D, const void *b,
                                const float *b_scales, int32_t n_groups, int64_t F, const int32_t *offsets, int act,
@@ -541,9 +542,9 @@ int mgs_quant_rows_i8(const void *x, int64_t M, int64_t K, void *q, float *scale
  *   b, b_scales  (n_groups, N, K) int8, (n_groups, N) fp32.
  *   offsets, out_type, y  as for mgs_mm_block128. Rows past the last end give
  *                zeros.
- * The scales are finite and positive. Requirements: N % 16 == 0, K % 16 == 0,
- * K <= MGS_I8_MAX_K, N < 2^21 - 64, n_groups <= MGS_MAX_GROUPS; a, b and y
- * 16-byte aligned. K == 0 gives zeros.
+ * The scales are finite and positive. Requirements: M < 2^31 - 256, N % 16 == 0,
+ * K % 16 == 0, K <= MGS_I8_MAX_K, N < 2^21 - 64, n_groups <= MGS_MAX_GROUPS; a, b
+ * and y 16-byte aligned. K == 0 gives zeros.
  */
 int mgs_mm_i8(const void *a, const float *a_scales, int64_t M, int64_t K, const void *b, const float *b_scales,
               int32_t n_groups, int64_t N, const int32_t *offsets, int out_type, void *y, void *stream);

@@ -1,6 +1,7 @@
 """CPU checks of the gated feed-forward and 8-bit integer calls: refusals of
 the C entry points before any GPU work, the Python front end, the form that
 each tested size takes, and the 64-bit forms that the GPU tests compare with."""
+import contextlib
 import inspect
 import subprocess
 
@@ -28,7 +29,7 @@ def L():
 OPERANDS = ("a", "sa", "M", "K", "b", "sb", "G", "N", "off")
 BAD = (dict(M=-1), dict(N=-16), dict(K=-16), dict(N=24), dict(K=24), dict(G=0), dict(G=-3), dict(off=None), dict(off=A + 2),
        dict(a=None), dict(a=A + 8), dict(b=None), dict(b=A + 8), dict(sa=None), dict(sa=A + 2), dict(sb=None), dict(sb=A + 1))
-LARGE = (dict(G=1025), dict(M=1 << 31), dict(N=1 << 31), dict(N=1 << 21), dict(K=1 << 23), dict(M=1 << 30, N=1 << 20))
+LARGE = (dict(G=1025), dict(M=1 << 31), dict(M=(1 << 31) - 256, N=16), dict(N=1 << 31), dict(N=1 << 21), dict(K=1 << 23), dict(M=1 << 30, N=1 << 20))
 
 
 def refusals(f, bad, large=LARGE):
@@ -111,10 +112,33 @@ def test_memory_of_outputs(taken, monkeypatch, name, stream):  # noqa: F811
     """Outputs are taken from the stream that the call runs on."""
     monkeypatch.setattr(feedforward, "_need", lambda *a, **kw: None)
     monkeypatch.setattr(feedforward, "lib", Library)
+    monkeypatch.setattr(feedforward, "_given", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)        # where CPU tensors say they are
     call, outputs = MEMORY[name]
     call(stream=Stream(SIDE) if stream == "object" else stream)
     assert [t.taken_on for t in taken] == [SIDE if stream else CURRENT] * outputs
     assert [t.recorded for t in taken] == [[CURRENT] if stream else []] * outputs
+
+
+@pytest.mark.parametrize("current", [-1, 3])
+def test_tensors_of_another_device(monkeypatch, current):
+    """A call makes its tensors' device the current one, and leaves it as it was."""
+    now, seen = [current], []
+
+    @contextlib.contextmanager
+    def device(d):
+        now.append(-1 if d == torch.device("cpu") else d)
+        yield
+        now.pop()
+
+    class Noting:
+        def __getattr__(self, name):
+            return lambda *a: seen.append(now[-1]) or mgs.MGS_OK
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[-1])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(feedforward, "lib", Noting)
+    feedforward._run("mgs_mm_i8", U8)
+    assert seen == [-1] and now == [current]
 
 
 PROGRAM = r"""

@@ -218,6 +218,19 @@ def test_two_calls_at_once():
         assert all(same(g, w) for g, w in zip(outs, want[n])), n
 
 
+@pytest.mark.parametrize("M,F,D,fast", [(9, 48, 144, False), (60, 272, 272, True), (700, 1200, 400, True), (2000, 1200, 144, False),
+                                        (2100, 2336, 144, True), (8200, 4000, 144, True)])
+def test_gradients_in_place_of_the_projections(M, F, D, fast):
+    """In every form, gu may be overwritten by its gradients."""
+    rng = np.random.default_rng(M)
+    gu = to_dev(wl.randn_bf16(rng, (M, 2 * F), 1.0)).view(torch.bfloat16)
+    dy = mgs.mgs_quant_rows128(to_dev(wl.randn_bf16(rng, (M, D), 1.0)).view(torch.bfloat16))
+    w = mgs.mgs_quant_blocks128(to_dev(wl.randn_bf16(rng, (1, F, D), 0.1)).view(torch.bfloat16), transposed=False)
+    want, h = feedforward.mgs_mm_gated_grad_block128(*dy, *w, gu, fast_accum=fast, hidden=True)
+    got, again = feedforward.mgs_mm_gated_grad_block128(*dy, *w, gu, fast_accum=fast, hidden=True, dgu=gu)
+    assert got is gu and same(got, want) and same(again, h)
+
+
 def test_front_end_refuses():
     c = calls()
     out = {n: f() for n, f in c.items()}
@@ -241,6 +254,7 @@ def test_front_end_refuses():
             (lambda: feedforward.mgs_quant_rows_i8(one), TypeError),
             (lambda: feedforward.mgs_quant_rows_i8(torch.zeros(64, dtype=torch.bfloat16, device="cuda")), ValueError),
             (lambda: feedforward.mgs_quant_rows_i8(torch.zeros((2, 12), dtype=torch.bfloat16, device="cuda")), mgs.MgsError),
+            (lambda: feedforward.mgs_mm_i8(torch.zeros(264, dtype=torch.int8, device="cuda")[8:].view(4, 64), one, w, sw), mgs.MgsError),
             (lambda: c["grad"](dgu=out["gated"][0]), ValueError)):
         with pytest.raises(error):
             call()

@@ -9,7 +9,7 @@ constexpr int kFewCols = 32;      // columns of a tile of the form for few rows
 
 struct MmForm {
     int few;      // rows of a tile of the form for few rows or few outputs, or 0:
-    int tile;     // tiles of 256 x 256 or 128 x 128 through LDS,
+    int tile;     // tiles of 256 x 256 or 128 x 128 through LDS (few rows: mm_form_rows),
     int sets;     // with this many sets of waves on one tile's contraction
 };
 
@@ -62,32 +62,39 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 }
 
 // Which form the gated products, their gradient and the 8-bit integer ones take; N
-// counts both projections' columns, `eight` that the instruction reads the bytes
-// themselves. Groups end inside tiles: half a row of tiles more for each.
-// - few rows: up to 20 a group one row of fragments, but tiles where enough
-//   weights are read that two workgroups a CU stream them as fast (16 tokens to 4
-//   of 64 experts, 2 x 2048 x 4096: 113, with few rows 119; one token to 2 x 8192 x
-//   5120: 35 and 16). Else the fewest rows a tile that leave one workgroup a CU
-//   (integers, 64 rows by 4096 x 4096: 11.4 with 32 rows, 14.9 with 64, 14.6 with
-//   16, 20.5 on tiles; gradient of 256 rows in 4 groups, 1040 x 4096: 19.7 and 29).
-//   Between them up to 40 rows of one group two rows of fragments (32 rows, 2 x 8192 x
-//   5120 in integers: 24.6, on tiles 27.9).
+// counts both projections' columns, `ints` and `eight` that operands are integers and
+// that the instruction reads the bytes themselves. In the form for few rows `tile` is
+// the lines of weights a tile has. Groups end inside tiles: half a row of tiles more
+// for each. (us, MI355X; I: integers, E: E4M3, X: E4M3 with binary32 sums.)
+// - the form for few rows with the smallest tile that leaves one workgroup a CU at
+//   most: its eight waves share a contraction however few tiles there are (I, 64 rows by
+//   4096 x 4096: 11.6 with 32 rows and 32 lines, 14.6 with 16, 20.5 on tiles of 128 x 128;
+//   1000 rows by 800 x 8192: 34 with 64 and 64, 37 on tiles; gradient of 256 rows,
+//   2048 x 4096: E 18 with 32 and 64, 28 on tiles, X 19 and 43; E has no registers for
+//   64 and 64). X takes 32 and 64 for two rounds of them too (64 rows, 2 x 8192 x 5120:
+//   39, on tiles 50; three rounds 56).
+// - up to 20 rows a group 16 rows a tile, whatever the weights: with 64 lines, which read a
+//   row half as often, for E and X (4 tokens to 2 of 16 experts of 2 x 8192 x 5120: 126,
+//   with 32 lines 144, on tiles 138), with 32 for I, whose waves then are twice as many
+//   a CU (122, with 64 lines 140, on tiles 124).
+// - up to 40 rows 32 and 64, for I only where there is one group (E, 64 tokens to 8 of 64
+//   experts of 2 x 2048 x 4096: 218, on tiles 234; I: 228 and 219).
 // - tiles of 256 x 256, one a CU, or 128 x 128, two a CU: by the time of their
 //   rounds, in hundredths of a round of two tiles of 128 x 128 a CU. A tile of
-//   256 x 256 takes 1.47 of it and one of 128 x 128 alone on its CU 0.65 (integers,
-//   2048 x 4096 x 4096: 37 on tiles of 128 and 52; 2048 rows in 8 groups: 69 and
-//   58; 4096 rows in 16 groups, 4112 x 4176: 187 and 164).
+//   256 x 256 takes 1.47 of it and one of 128 x 128 alone on its CU 0.65 (I, 2048 x
+//   4096 x 4096: 37 on tiles of 128 and 52; 2048 rows in 8 groups: 69 and 58; 4096
+//   rows in 16 groups, 4112 x 4176: 187 and 164).
 // - two sets of waves on a tile of 128 x 128 where there is one a CU at most (256 rows,
 //   2 x 8192 x 5120: 33, one set 39; with 264 tiles 52 and 37).
-inline MmForm mm_form_rows(bool eight, bool grouped, int64_t M, int64_t N, int64_t G, int cus) {
+inline MmForm mm_form_rows(bool ints, bool eight, bool grouped, int64_t M, int64_t N, int64_t G, int cus) {
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t groups = grouped ? G : 1, extra = grouped ? G / 2 : 0, rows = up(M, groups);
-    const int64_t used = groups < up(M, 16) ? groups : up(M, 16);      // groups that can have rows
-    if (rows <= 20 && !(eight && used * up(N, 128) >= 4 * cus)) return {16, 0, 0};
-    for (int few = 16; few <= 64; few *= 2)
-        if ((up(M, few) + extra) * up(N, kFewCols) <= cus) return {few, 0, 0};
-    if (groups == 1 && rows <= 40) return {32, 0, 0};
-    if (!eight) return {0, 128, 1};
+    constexpr int kFew[5][2] = {{16, 32}, {32, 32}, {16, 64}, {32, 64}, {64, 64}};
+    for (int i = 0; i < (ints ? 5 : 4); ++i)
+        if ((up(M, kFew[i][0]) + extra) * up(N, kFew[i][1]) <= cus) return {kFew[i][0], kFew[i][1], 0};
+    if (rows <= 20) return {16, ints ? 32 : 64, 0};
+    if (rows <= 40 && (groups == 1 || !ints)) return {32, 64, 0};
+    if (!eight) return (up(M, 32) + extra) * up(N, 64) <= 2 * cus ? MmForm{32, 64, 0} : MmForm{0, 128, 1};
     const int64_t large = (up(M, 256) + extra) * up(N, 256), small = (up(M, 128) + extra) * up(N, 128);
     if (small <= cus) return {0, 128, 2};
     const int64_t left = small % (2 * cus);

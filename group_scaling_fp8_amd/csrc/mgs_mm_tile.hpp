@@ -989,16 +989,16 @@ __device__ __forceinline__ v8i load32(const uint8_t* p, int64_t at, int64_t len)
     return __builtin_shufflevector(first ? lo : zero, second ? hi : zero, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int BM, class KIND>
+template <int BM, int LINES, class KIND>
 __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     constexpr bool WGRAD = KIND::wgrad, GATED = KIND::gated, GRAD = KIND::grad, F32 = KIND::f32;
     constexpr bool SCALED = KIND::scaled, INT8 = KIND::num == Num::Int8;
-    constexpr int MT = BM / 16, NT = kFewCols / 16;
-    constexpr int COLS = GATED ? kFewCols / 2 : kFewCols;      // gated: 16 columns of both projections
+    constexpr int MT = BM / 16, NT = LINES / 16;
+    constexpr int COLS = GATED ? LINES / 2 : LINES;            // gated: the same columns of both projections
     constexpr int BLOCKS = GATED ? 2 : 1;                      // weights that have scales of their own
     using Op = Operand<KIND::num>;
     using Acc = typename Sum<INT8>::type;
-    __shared__ __align__(16) float s_sum[kFewWaves][BM][kFewCols + 4];
+    __shared__ __align__(16) float s_sum[kFewWaves][BM][LINES + 4];
     const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)(threadIdx.x / kWave));
     const int64_t nnb = (p.N + 127) / 128;
     const int col_tiles = (int)((p.cols + COLS - 1) / COLS), M = (int)p.M;
@@ -1123,7 +1123,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        acc[i][j][c] = fmaf(part[j][c], f[i][GATED ? j : 0], acc[i][j][c]);
+                        acc[i][j][c] = fmaf(part[j][c], f[i][GATED ? j / (NT / 2) : 0], acc[i][j][c]);
             }
         }
     };
@@ -1144,9 +1144,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int64_t r = min((int64_t)t.n0 + (GATED ? 0 : j * 16) + fr, p.cols - 1);
+            const int64_t r = min((int64_t)t.n0 + (GATED ? j % (NT / 2) : j) * 16 + fr, p.cols - 1);
             pb[j] = WGRAD ? p.b + r * stride + t.begin
-                          : p.b + (((int64_t)t.g * BLOCKS + (GATED ? j : 0)) * p.N + r) * stride;
+                          : p.b + (((int64_t)t.g * BLOCKS + (GATED ? j / (NT / 2) : 0)) * p.N + r) * stride;
         }
         if (wave < nkb) fetch(x, wave);
     };
@@ -1253,17 +1253,17 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     }
 }
 
-template <int BM, class KIND>
+template <int BM, int LINES, class KIND>
 hipError_t launch_few(const MmArgs& p, int cus, hipStream_t stream) {
     constexpr bool WGRAD = KIND::wgrad;
-    constexpr int COLS = KIND::gated ? kFewCols / 2 : kFewCols;
+    constexpr int COLS = KIND::gated ? LINES / 2 : LINES;
     const int64_t groups = p.offsets ? p.G + 1 : 1, spare = groups < p.M ? groups : p.M;
     const int64_t down = WGRAD ? p.G * ((p.N + BM - 1) / BM) : (p.M + spare * (BM - 1)) / BM;
     const int64_t tiles = down * ((p.cols + COLS - 1) / COLS);
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
     const int64_t most = cus * (BM == 16 ? 16 : 8) / kFewWaves;
     const int64_t blocks = WGRAD || tiles < most ? tiles : most;
-    hipLaunchKernelGGL((mm_few_kernel<BM, KIND>), grid_xz(blocks), dim3(kFewWaves * 64), 0, stream, p);
+    hipLaunchKernelGGL((mm_few_kernel<BM, LINES, KIND>), grid_xz(blocks), dim3(kFewWaves * 64), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -1288,11 +1288,19 @@ template <class KIND>
 hipError_t launch_sized(const MmArgs& p, int cus, hipStream_t stream) {
     const bool grouped = p.offsets != nullptr;
     const MmForm form = KIND::halves
-                            ? mm_form_rows(KIND::eight, grouped, p.M, (KIND::gated ? 2 : 1) * p.N, p.G, cus)
+                            ? mm_form_rows(KIND::num == Num::Int8, KIND::eight, grouped, p.M, (KIND::gated ? 2 : 1) * p.N, p.G, cus)
                             : mm_form(KIND::wgrad, KIND::eight, grouped, p.M, p.N, p.K, p.G, cus);
-    if (form.few == 16) return launch_few<16, typename KIND::few>(p, cus, stream);
-    if (form.few == 32) return launch_few<32, typename KIND::few>(p, cus, stream);
-    if (form.few == 64) return launch_few<64, typename KIND::few>(p, cus, stream);
+    using Few = typename KIND::few;
+    if constexpr (KIND::halves) {
+        if (form.few == 16 && form.tile == 64) return launch_few<16, 64, Few>(p, cus, stream);
+        if (form.few == 32 && form.tile == 64) return launch_few<32, 64, Few>(p, cus, stream);
+        if constexpr (KIND::num == Num::Int8)
+            if (form.few == 64) return launch_few<64, 64, Few>(p, cus, stream);
+    } else {
+        if (form.few == 64) return launch_few<64, 32, Few>(p, cus, stream);
+    }
+    if (form.few == 16) return launch_few<16, 32, Few>(p, cus, stream);
+    if (form.few == 32) return launch_few<32, 32, Few>(p, cus, stream);
     if constexpr (KIND::wgrad || KIND::eight) {
         if (form.tile == 256) return launch<256, 256, 128, 64, 1, KIND>(p, cus, stream);
         if (form.sets == 2) return launch<128, 128, 64, 64, 2, KIND>(p, cus, stream);

@@ -145,9 +145,9 @@ PROGRAM = r"""
 #include <stdio.h>
 #include "mgs_mm_form.hpp"
 int main() {
-    long long eight, grouped, M, N, G, cus;
-    while (scanf("%lld %lld %lld %lld %lld %lld", &eight, &grouped, &M, &N, &G, &cus) == 6) {
-        const mgs::MmForm f = mgs::mm_form_rows(eight, grouped, M, N, G, (int)cus);
+    long long ints, eight, grouped, M, N, G, cus;
+    while (scanf("%lld %lld %lld %lld %lld %lld %lld", &ints, &eight, &grouped, &M, &N, &G, &cus) == 7) {
+        const mgs::MmForm f = mgs::mm_form_rows(ints, eight, grouped, M, N, G, (int)cus);
         printf("%d %d %d\n", f.few, f.tile, f.sets);
     }
     return 0;
@@ -171,20 +171,34 @@ def form(tmp_path_factory):
 @pytest.mark.parametrize("gated,case", [(False, c) for c in ROWS] + [(True, c) for c in GATED])
 def test_sizes_take_their_forms(form, gated, case):
     """So that a changed rule cannot take a form out of the GPU tests unseen."""
-    M, N, K, G, kind, eight, exact = case
+    M, N, K, G, kind, ints, fast, exact = case
     N *= 2 if gated else 1
-    assert form(1, kind != "none", M, N, G, CUS) == eight
-    assert form(0, kind != "none", M, N, G, CUS) == exact
+    assert form(1, 1, kind != "none", M, N, G, CUS) == ints
+    assert form(0, 1, kind != "none", M, N, G, CUS) == fast
+    assert form(0, 0, kind != "none", M, N, G, CUS) == exact
+
+
+def test_every_form_is_tested():
+    few = {(rows, lines, 0) for rows in (16, 32) for lines in (32, 64)}
+    tiles = {(0, 128, 1), (0, 128, 2), (0, 256, 1)}
+    for cases in (ROWS, GATED):
+        assert {c[5] for c in cases} == few | {(64, 64, 0)} | tiles
+        assert {c[6] for c in cases} == few | tiles
+        assert {c[7] for c in cases} == few | {(0, 128, 1)}
 
 
 def test_limits_between_the_forms(form):
     for args, want in (
-            ((1, 0, 1, 8192, 1), (16, 0, 0)), ((1, 0, 20, 16384, 1), (16, 0, 0)), ((1, 0, 21, 16384, 1), (32, 0, 0)),
-            ((1, 0, 41, 16384, 1), (0, 128, 2)), ((1, 1, 128, 16384, 16), (0, 128, 1)), ((0, 1, 128, 16384, 16), (16, 0, 0)),
-            ((1, 1, 32, 16384, 16), (16, 0, 0)), ((1, 0, 64, 4096, 1), (32, 0, 0)), ((1, 0, 128, 4096, 1), (64, 0, 0)),
-            ((1, 0, 256, 16384, 1), (0, 128, 2)), ((0, 0, 256, 16384, 1), (0, 128, 1)), ((1, 1, 256, 1040, 4), (64, 0, 0)),
-            ((1, 0, 2048, 4096, 1), (0, 128, 1)), ((1, 1, 2048, 4096, 8), (0, 256, 1)), ((1, 0, 1003, 4176, 1), (0, 128, 1)),
-            ((1, 1, 16640, 16384, 16), (0, 256, 1)), ((1, 0, 2147483647, 2097088, 1), (0, 256, 1))):
+            ((1, 1, 0, 1, 8192, 1), (16, 32, 0)), ((1, 1, 0, 1, 16400, 1), (16, 32, 0)), ((0, 1, 0, 1, 16400, 1), (16, 64, 0)),
+            ((1, 1, 0, 1, 16384, 1), (16, 64, 0)), ((1, 1, 0, 32, 16384, 1), (32, 64, 0)), ((1, 1, 0, 33, 16384, 1), (64, 64, 0)),
+            ((0, 1, 0, 33, 16384, 1), (32, 64, 0)), ((0, 1, 0, 41, 16384, 1), (0, 128, 2)), ((0, 0, 0, 64, 16384, 1), (32, 64, 0)),
+            ((0, 0, 0, 65, 16384, 1), (0, 128, 1)), ((0, 0, 0, 512, 2048, 1), (32, 64, 0)), ((0, 0, 0, 513, 2048, 1), (0, 128, 1)), ((1, 1, 0, 65, 16384, 1), (0, 128, 2)), ((1, 1, 1, 320, 16384, 16), (16, 32, 0)),
+            ((0, 1, 1, 320, 16384, 16), (16, 64, 0)), ((0, 1, 1, 640, 16384, 16), (32, 64, 0)), ((1, 1, 1, 640, 16384, 16), (0, 128, 1)),
+            ((0, 0, 1, 640, 16384, 16), (32, 64, 0)), ((0, 0, 1, 641, 16384, 16), (0, 128, 1)), ((1, 1, 0, 64, 4096, 1), (32, 32, 0)),
+            ((1, 1, 0, 128, 4096, 1), (32, 64, 0)), ((1, 1, 0, 256, 16384, 1), (0, 128, 2)), ((0, 0, 0, 256, 16384, 1), (0, 128, 1)),
+            ((0, 1, 1, 256, 1040, 4), (32, 64, 0)), ((1, 1, 0, 2048, 4096, 1), (0, 128, 1)), ((1, 1, 1, 2048, 4096, 8), (0, 256, 1)),
+            ((1, 1, 0, 1003, 4176, 1), (0, 128, 1)), ((1, 1, 1, 16640, 16384, 16), (0, 256, 1)),
+            ((1, 1, 0, 2147483391, 2097072, 1), (0, 256, 1)), ((1, 1, 1, 1, 16, 1024), (16, 32, 0))):
         assert form(*args, CUS) == want, args
 
 

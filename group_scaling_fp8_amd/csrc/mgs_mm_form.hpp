@@ -74,9 +74,10 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 //   64 and 64). X takes 32 and 64 for two rounds of them too (64 rows, 2 x 8192 x 5120:
 //   39, on tiles 50; three rounds 56).
 // - up to 20 rows a group 16 rows a tile, whatever the weights: with 64 lines, which read a
-//   row half as often, for E and X (4 tokens to 2 of 16 experts of 2 x 8192 x 5120: 126,
-//   with 32 lines 144, on tiles 138), with 32 for I, whose waves then are twice as many
-//   a CU (122, with 64 lines 140, on tiles 124).
+//   row half as often (E, 4 tokens to 2 of 16 experts of 2 x 8192 x 5120: 116, with 32
+//   lines 134, on tiles 136; I: 117, 122 and 123), but with 32 for I of short rows, which
+//   have too few blocks a wave (16 tokens to 4 of 64 experts of 2 x 2048 x 4096: 115 and
+//   103; E 110 and 119).
 // - up to 40 rows 32 and 64, for I only where there is one group (E, 64 tokens to 8 of 64
 //   experts of 2 x 2048 x 4096: 218, on tiles 234; I: 228 and 219).
 // - tiles of 256 x 256, one a CU, or 128 x 128, two a CU: by the time of their
@@ -86,13 +87,13 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 //   rows in 16 groups, 4112 x 4176: 187 and 164).
 // - two sets of waves on a tile of 128 x 128 where there is one a CU at most (256 rows,
 //   2 x 8192 x 5120: 33, one set 39; with 264 tiles 52 and 37).
-inline MmForm mm_form_rows(bool ints, bool eight, bool grouped, int64_t M, int64_t N, int64_t G, int cus) {
+inline MmForm mm_form_rows(bool ints, bool eight, bool grouped, int64_t M, int64_t N, int64_t K, int64_t G, int cus) {
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t groups = grouped ? G : 1, extra = grouped ? G / 2 : 0, rows = up(M, groups);
     constexpr int kFew[5][2] = {{16, 32}, {32, 32}, {16, 64}, {32, 64}, {64, 64}};
     for (int i = 0; i < (ints ? 5 : 4); ++i)
         if ((up(M, kFew[i][0]) + extra) * up(N, kFew[i][1]) <= cus) return {kFew[i][0], kFew[i][1], 0};
-    if (rows <= 20) return {16, ints ? 32 : 64, 0};
+    if (rows <= 20) return {16, ints && K < 5120 ? 32 : 64, 0};
     if (rows <= 40 && (groups == 1 || !ints)) return {32, 64, 0};
     if (!eight) return (up(M, 32) + extra) * up(N, 64) <= 2 * cus ? MmForm{32, 64, 0} : MmForm{0, 128, 1};
     const int64_t large = (up(M, 256) + extra) * up(N, 256), small = (up(M, 128) + extra) * up(N, 128);

@@ -130,8 +130,11 @@ def mgs_quant_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scales:
     _need(x, "x", _BF16_LIKE)
     if x.dim() not in (2, 3):
         raise ValueError("x must have 2 or 3 dims")
-    q = _out(q, tuple(x.shape), torch.int8, x.device, "q", stream)
-    scales = _out(scales, tuple(x.shape[:-1]), torch.float32, x.device, "scales", stream)
+    if q is None and scales is None and stream is None:      # the cheapest way to both: one token's cast takes 2 us
+        q, scales = torch.empty_like(x, dtype=torch.int8), x.new_empty(x.shape[:-1], dtype=torch.float32)
+    else:
+        q = _out(q, tuple(x.shape), torch.int8, x.device, "q", stream)
+        scales = _out(scales, tuple(x.shape[:-1]), torch.float32, x.device, "scales", stream)
     _run("mgs_quant_rows_i8", x, x.data_ptr(), scales.numel(), x.shape[-1], q.data_ptr(), scales.data_ptr(),
          _stream_handle(stream, x))
     return q, scales

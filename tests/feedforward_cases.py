@@ -19,6 +19,8 @@ ROWS = [
     (48, 144, 144, 2, "empty", FEW16_32, FEW16_32, FEW16_32),
     (20, 16448, 144, 1, "none", FEW16_32, FEW16_64, FEW16_64),
     (19, 8256, 1296, 1, "even", FEW32_64, FEW32_64, FEW32_64),
+    (18, 16448, 5136, 1, "none", FEW16_64, FEW16_64, FEW16_64),
+    (40, 32912, 5136, 2, "even", FEW16_64, FEW16_64, FEW16_64),
     (33, 4064, 144, 1, "none", FEW32_32, FEW32_32, FEW32_32),
     (600, 272, 528, 5, "tail", FEW32_32, FEW32_32, FEW32_32),
     (900, 144, 144, 6, "bad", FEW32_32, FEW32_32, FEW32_32),

@@ -9,6 +9,15 @@
 // integers, which hold 131071 products of any two bytes. A sum is rounded to
 // binary32 once and scaled once, so a result does not depend on the form, the
 // tile or the order of its sum.
+//
+// The products are the tiles of mgs_mm_tile.hpp with sums in place: two 16 x 16 x 64
+// instructions for a step's 128 bytes, scales once at the end. Dense products run at
+// 2623 TOP/s (16384^3; the library's at 2391), the gated pair at 2586 (16384 x 2 x
+// 8192 x 8192), bound by the matrix cores; in 16 ragged groups (16640 rows, 2 x 8192
+// x 5120) 1335 us, of which the rows of tiles past a group's end are 12%. One row by
+// 8192 x 8192 13 us, bound by the weights' bytes at 5.1 TB/s. Rows whose length is no
+// multiple of 128 cross a line in every step: 4096 rows in 16 groups by 4096 x 4176
+// take 164 us, by 4096 x 4096 126.
 #include "mgs_experts.hpp"
 #include "mgs_kernels.hpp"
 #include "mgs_mm_tile.hpp"
@@ -42,22 +51,28 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* s_max) {
         m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
     }
     if constexpr (LANES > kWave) {
-        static_assert(LANES == 256, "one row a workgroup");
         __syncthreads();             // the last row's maxima are read
         if ((threadIdx.x & (kWave - 1)) == 0) s_max[threadIdx.x / kWave] = m;
         __syncthreads();
-        m = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+        m = s_max[0];
+#pragma unroll
+        for (int w = 1; w < LANES / kWave; ++w) m = max(m, s_max[w]);
     }
     return m;
 }
 
-// LANES threads cast a row; up to LANES * V * 8 columns stay in registers
-// between the maximum and the cast (HELD), longer rows are read again.
+// Threads of a workgroup where LANES of them cast a row.
+template <int LANES>
+constexpr int kThreads = LANES > 256 ? LANES : 256;
+
+// LANES threads cast a row; up to LANES * V * 8 columns stay in registers between the
+// maximum and the cast (HELD), longer rows are read again. Bound by memory: 16640 x
+// 8192, 0.41 GB, 61 us, 6.7 TB/s.
 template <int LANES, int V, bool HELD>
-__global__ __launch_bounds__(256) void rows_i8_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+__global__ __launch_bounds__(kThreads<LANES>) void rows_i8_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                       uint8_t* __restrict__ q, float* __restrict__ scales) {
-    __shared__ uint32_t s_max[4];
-    constexpr int ROWS = 256 / LANES;
+    __shared__ uint32_t s_max[kThreads<LANES> / kWave];
+    constexpr int ROWS = kThreads<LANES> / LANES;
     const int lane = threadIdx.x % LANES;
     for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < M; r0 += (int64_t)gridDim.x * ROWS) {
         const int64_t r = r0 + threadIdx.x / LANES;
@@ -93,21 +108,28 @@ __global__ __launch_bounds__(256) void rows_i8_kernel(const uint16_t* __restrict
 
 template <int LANES, int V, bool HELD>
 hipError_t launch_rows(const uint16_t* x, int64_t M, int64_t K, uint8_t* q, float* scales, hipStream_t stream) {
-    constexpr int ROWS = 256 / LANES;
+    constexpr int ROWS = kThreads<LANES> / LANES;
     const int64_t want = (M + ROWS - 1) / ROWS, blocks = want < (1 << 20) ? want : (1 << 20);
-    hipLaunchKernelGGL((rows_i8_kernel<LANES, V, HELD>), dim3((unsigned)blocks), dim3(256), 0, stream, x, M, K, q,
-                       scales);
+    hipLaunchKernelGGL((rows_i8_kernel<LANES, V, HELD>), dim3((unsigned)blocks), dim3(kThreads<LANES>), 0, stream, x, M,
+                       K, q, scales);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// The fewest lanes whose registers hold a row (us of 136 M values, MI355X): rows of 512
+// with 16 lanes 62, with 64 73; of 2048 with 64 61, with 256 73; of 2560 with 64 lanes of
+// eight pieces 62, with 256 of four 67; of 32768 with 256 lanes 63, read twice 103; of
+// 65536 with 1024 lanes 72, read twice 103.
 hipError_t launch_rows_i8(const uint16_t* x, int64_t M, int64_t K, uint8_t* q, float* scales, hipStream_t stream) {
     if (K <= 512) return launch_rows<16, 4, true>(x, M, K, q, scales, stream);
     if (K <= 2048) return launch_rows<64, 4, true>(x, M, K, q, scales, stream);
+    if (K <= 4096) return launch_rows<64, 8, true>(x, M, K, q, scales, stream);
     if (K <= 8192) return launch_rows<256, 4, true>(x, M, K, q, scales, stream);
     if (K <= 16384) return launch_rows<256, 8, true>(x, M, K, q, scales, stream);
-    return launch_rows<256, 8, false>(x, M, K, q, scales, stream);
+    if (K <= 32768) return launch_rows<256, 16, true>(x, M, K, q, scales, stream);
+    if (K <= 131072) return launch_rows<1024, 16, true>(x, M, K, q, scales, stream);      // every length a product takes
+    return launch_rows<1024, 8, false>(x, M, K, q, scales, stream);
 }
 
 hipError_t launch_mm_i8(const uint8_t* a, const float* a_scales, int64_t M, int64_t K, const uint8_t* b,

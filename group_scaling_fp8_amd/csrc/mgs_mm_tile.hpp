@@ -371,9 +371,13 @@ __device__ __forceinline__ void wait_some_or_none(int some) {
 //                     its second step on, each wait is for all that came before.
 //                     Short contractions (eight steps a tile: wgrad of 16640 rows
 //                     in 16 groups) pay for output and sums one after the other.
-//   few tiles         latency: two steps' loads (64 KiB a CU) are in flight. 128 x
-//                     128 tiles of 4096 rows in 16 groups by 4096 x 4096 take in 39
-//                     KB/us a CU, with the matrix cores busy 26% of the time.
+//   few tiles         128 x 128 tiles of 4096 rows in 16 groups by 4096 x 4096 take in
+//                     39 KB/us a CU, with the matrix cores busy 26% of the time. Where
+//                     a CU has one workgroup, a wave a SIMD waits for its own reads of
+//                     LDS: 256 x 4096 x 4096 in integers takes 25.7 us, 24.9 with the
+//                     loads from memory left out, and deeper buffers (four steps) gain
+//                     nothing.
+//   epilogues         of a gated pair and its gradient: mgs_gated.hip.
 // (The clock falls as the matrix cores are used more: 1.9 to 2.0 GHz in the large
 // products here, 1.5 to 1.6 under the library's.)
 template <int BM, int BN, int WM, int WN, int PARTS, class KIND>
@@ -968,14 +972,18 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
 
 // ---- few output rows, or few outputs of a long contraction -----------------------
 //
-// With a handful of rows the weights' bytes are block128's whole cost, and with a
-// small weight wgrad has few tiles of a long contraction: a tile is BM rows by 32
-// columns, and its eight waves take the contraction's blocks in turn (wave w: w,
-// w + 8, ...), so that even one small product has enough loads in flight on every
-// CU. Fragments come straight from memory, four lanes a line, the next block's
-// while this one is multiplied; sums are exact (the matrix cores have nothing else
-// to do). The waves' sums meet in LDS and are added in wave order. Bound by the
-// loads: one row by 8192 x 8192 17 us, 4 TB/s.
+// With a handful of rows the weights' bytes are a product's whole cost, and with a
+// small weight there are few tiles of a long contraction: a tile is BM rows by LINES
+// rows of weights (gated: half of them of each projection), and its eight waves take
+// the contraction's blocks in turn (wave w: w, w + 8, ...), so that even one small
+// product has enough loads in flight on every CU. Fragments come straight from memory,
+// four lanes a line, DEPTH blocks while one is multiplied; block128 and wgrad sum
+// exactly (the matrix cores have nothing else to do). The waves' sums meet in LDS and
+// are added in wave order. Workgroups walk tiles (wgrad: one each) and load the next
+// one's first blocks before they join (decode of four tokens in integers 143 to 121
+// us). A lane takes 16 bytes of both halves of a line; block128 and wgrad, whose order
+// of sums stays, 32 in a row. Bound by the loads: one row by 8192 x 8192 17 us in
+// E4M3, 13 in integers, 5.1 TB/s.
 constexpr int kFewWaves = 8;
 
 // The 16 bytes at p + at and those at APART bytes from them, of a row of len bytes

@@ -25,7 +25,8 @@ def _need_gpu():
 
 # every width class of the cast and its edges; rows that do not fill a workgroup
 @pytest.mark.parametrize("M,K", [(1, 8), (5, 16), (17, 120), (33, 512), (7, 520), (1, 2048), (9, 2056), (3, 5120), (2, 8192),
-                                 (5, 8200), (2, 16384), (3, 16392), (2, 40000), (1, 131056), (1000, 136)])
+                                 (5, 8200), (2, 16384), (3, 16392), (2, 32768), (2, 40000), (1, 131056), (1, 131072), (2, 131080),
+                                 (1, 300000), (1000, 136), (6, 4096), (5, 4104)])
 def test_cast(M, K):
     rng = np.random.default_rng(M + K)
     x = wl.randn_bf16(rng, (M, K), 0.5, 0.01, 20.0)

@@ -1166,6 +1166,35 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     const int64_t row_end = WGRAD ? p.N : t.end;
     const int g = t.g, m0 = t.m0, n0 = t.n0;
     const bool none = len == 0;
+    // A thread stores four columns of one or two rows. What their results take besides the
+    // sums is loaded first: at the end it would come behind the next tile's blocks.
+    constexpr int PIECES = BM * COLS / 4, TURNS = (PIECES + kFewWaves * 64 - 1) / (kFewWaves * 64);
+    auto piece = [&](int turn, int& r, int& c) {
+        const int x = threadIdx.x + turn * (kFewWaves * 64);
+        r = x / (COLS / 4);
+        c = x % (COLS / 4) * 4;
+        return x < PIECES && m0 + r < row_end && n0 + c < p.cols;
+    };
+    float sa[INT8 ? TURNS : 1], sb[INT8 ? TURNS : 1][BLOCKS][4];
+    uint2 kept[GRAD ? TURNS : 1][2];
+#pragma unroll
+    for (int turn = 0; turn < TURNS; ++turn) {
+        int r, c;
+        if (!piece(turn, r, c) || g < 0) continue;
+        if constexpr (INT8) {
+            sa[turn] = p.a_scales[m0 + r];
+#pragma unroll
+            for (int w = 0; w < BLOCKS; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sb[turn][w][i] = p.b_scales[((int64_t)g * BLOCKS + w) * p.N + n0 + c + i];
+        }
+        if constexpr (GRAD) {
+            const uint16_t* gu = p.gu + (int64_t)(m0 + r) * 2 * p.cols + n0 + c;
+            kept[turn][0] = *reinterpret_cast<const uint2*>(gu);
+            kept[turn][1] = *reinterpret_cast<const uint2*>(gu + p.cols);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -1203,7 +1232,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
         return __builtin_convertvector(v, v4f);
     };
     // and the scales that are not in the sums yet, of output columns col to col + 3 of weight w
-    auto scaled = [&](v4f v, int64_t row, int64_t col, int w) {
+    auto scaled = [&](v4f v, int64_t row, int64_t col, int turn, int w) {
         if constexpr (WGRAD) {
             if (!none) {
                 const float ia = 1.0f / p.a_scales[row * p.G + g];
@@ -1212,10 +1241,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
             }
         } else if constexpr (INT8) {
             if (g >= 0) {
-                const float ia = 1.0f / p.a_scales[row];
-                const float* sb = p.b_scales + ((int64_t)g * BLOCKS + w) * p.N + col;
+                const float ia = 1.0f / sa[turn];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = v[i] * ia * (1.0f / sb[i]);
+                for (int i = 0; i < 4; ++i) v[i] = v[i] * ia * (1.0f / sb[turn][w][i]);
             }
         }
         return v;
@@ -1223,14 +1251,15 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     auto store4 = [](void* out, int64_t at, v4f v) {
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
     };
-    for (int x = threadIdx.x; x < BM * COLS / 4; x += kFewWaves * 64) {
-        const int r = x / (COLS / 4), c = x % (COLS / 4) * 4;
-        if (m0 + r >= row_end || n0 + c >= p.cols) continue;
+#pragma unroll
+    for (int turn = 0; turn < TURNS; ++turn) {
+        int r, c;
+        if (!piece(turn, r, c)) continue;
         const int64_t row = m0 + r, col = n0 + c;
-        v4f v = scaled(joined(r, c), row, col, 0);
+        v4f v = scaled(joined(r, c), row, col, turn, 0);
         const int64_t at = row * p.cols + col, at2 = at + row * p.cols;
         if constexpr (GATED) {
-            const v4f u = scaled(joined(r, COLS + c), row, col, 1);
+            const v4f u = scaled(joined(r, COLS + c), row, col, turn, 1);
             if constexpr (KIND::more) {
                 store4(p.more, at2, v);
                 store4(p.more, at2 + p.cols, u);
@@ -1239,7 +1268,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
             for (int i = 0; i < 4; ++i) v[i] = p.act.of(v[i]) * u[i];
             store4(p.out, at, v);
         } else if constexpr (GRAD) {
-            const uint2 gw = *reinterpret_cast<const uint2*>(p.gu + at2), uw = *reinterpret_cast<const uint2*>(p.gu + at2 + p.cols);
+            const uint2 gw = kept[turn][0], uw = kept[turn][1];
             const float gs[4] = {bf16_lo(gw.x), bf16_hi(gw.x), bf16_lo(gw.y), bf16_hi(gw.y)};
             const float us[4] = {bf16_lo(uw.x), bf16_hi(uw.x), bf16_lo(uw.y), bf16_hi(uw.y)};
             v4f dg = {}, du = {}, h = {};

@@ -75,11 +75,11 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 //   39, on tiles 50; three rounds 56).
 // - up to 20 rows a group 16 rows a tile, whatever the weights: with 64 lines, which read a
 //   row half as often (E, 4 tokens to 2 of 16 experts of 2 x 8192 x 5120: 116, with 32
-//   lines 134, on tiles 136; I: 117, 122 and 123), but with 32 for I of short rows, which
-//   have too few blocks a wave (16 tokens to 4 of 64 experts of 2 x 2048 x 4096: 115 and
-//   103; E 110 and 119).
+//   lines 134, on tiles 137; I: 111, 121 and 125), but with 32 for I of short rows, which
+//   have too few blocks a wave (16 tokens to 4 of 64 experts of 2 x 2048 x 4096: 99, with
+//   64 lines 110; E 111 and 110).
 // - up to 40 rows 32 and 64, for I only where there is one group (E, 64 tokens to 8 of 64
-//   experts of 2 x 2048 x 4096: 218, on tiles 234; I: 228 and 219).
+//   experts of 2 x 2048 x 4096: 218, on tiles 234; I, more tokens a group: 277 and 269).
 // - tiles of 256 x 256, one a CU, or 128 x 128, two a CU: by the time of their
 //   rounds, in hundredths of a round of two tiles of 128 x 128 a CU. A tile of
 //   256 x 256 takes 1.47 of it and one of 128 x 128 alone on its CU 0.65 (I, 2048 x

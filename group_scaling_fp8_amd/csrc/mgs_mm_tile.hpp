@@ -1306,7 +1306,7 @@ hipError_t launch_few(const MmArgs& p, int cus, hipStream_t stream) {
     const int64_t tiles = down * ((p.cols + COLS - 1) / COLS);
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
     // Two blocks ahead pay for integers only, which have the registers (4 tokens to 2 of
-    // 16 experts, 2 x 8192 x 5120: 139 to 117 us; E4M3 116 to 125).
+    // 16 experts, 2 x 8192 x 5120: 140 to 117 us at the time; E4M3 116 to 125).
     constexpr int DEPTH = KIND::num == Num::Int8 && BM == 16 && LINES == 64 ? 2 : 1;
     const int64_t most = cus * (BM == 16 && LINES == 32 ? 16 : 8) / kFewWaves;       // by registers
     const int64_t blocks = WGRAD || tiles < most ? tiles : most;
@@ -1335,7 +1335,8 @@ template <class KIND>
 hipError_t launch_sized(const MmArgs& p, int cus, hipStream_t stream) {
     const bool grouped = p.offsets != nullptr;
     const MmForm form = KIND::halves
-                            ? mm_form_rows(KIND::num == Num::Int8, KIND::eight, grouped, p.M, (KIND::gated ? 2 : 1) * p.N, p.K, p.G, cus)
+                            ? mm_form_rows(KIND::num == Num::Int8, KIND::eight, grouped, p.M,
+                                           (KIND::gated ? 2 : 1) * p.N, p.K, p.G, cus)
                             : mm_form(KIND::wgrad, KIND::eight, grouped, p.M, p.N, p.K, p.G, cus);
     using Few = typename KIND::few;
     if constexpr (KIND::halves) {

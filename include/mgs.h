@@ -530,14 +530,15 @@ int mgs_mm_gated_grad_block128(const void *dy, const float *dy_scales, int64_t M
  * One scale for each row: x (M, K) bf16, scales (M) fp32 = fl32(127 /
  * max(amax, 1e-12)), q (M, K) int8 = fl32(x * scale) rounded to the nearest
  * integer, ties to even: -127 to 127. x is finite. The weights of E experts
- * (E, N, K) are E * N rows. Requirements: K % 8 == 0; x 16-byte aligned, q
- * 8-byte aligned. M == 0 or K == 0 is a no-op.
+ * (E, N, K) are E * N rows. Requirements: M and K < 2^31, K % 8 == 0; x 16-byte
+ * aligned, q 8-byte aligned. M == 0 or K == 0 is a no-op.
  */
 int mgs_quant_rows_i8(const void *x, int64_t M, int64_t K, void *q, float *scales, void *stream);
 
 /*
  * For m in group e: y[m, n] = sum_k a[m, k] * b[e, n, k] / (a_scales[m] *
- * b_scales[e, n]); the sum is exact and rounded to fp32 before it is scaled.
+ * b_scales[e, n]); the sum is exact and rounded to fp32 before it is divided by
+ * a_scales[m], which fp32 has to hold, and then by b_scales[e, n].
  *   a, a_scales  (M, K) int8, (M) fp32.
  *   b, b_scales  (n_groups, N, K) int8, (n_groups, N) fp32.
  *   offsets, out_type, y  as for mgs_mm_block128. Rows past the last end give

@@ -27,9 +27,11 @@ def L():
 
 
 OPERANDS = ("a", "sa", "M", "K", "b", "sb", "G", "N", "off")
-BAD = (dict(M=-1), dict(N=-16), dict(K=-16), dict(N=24), dict(K=24), dict(G=0), dict(G=-3), dict(off=None), dict(off=A + 2),
-       dict(a=None), dict(a=A + 8), dict(b=None), dict(b=A + 8), dict(sa=None), dict(sa=A + 2), dict(sb=None), dict(sb=A + 1))
-LARGE = (dict(G=1025), dict(M=1 << 31), dict(M=(1 << 31) - 256, N=16), dict(N=1 << 31), dict(N=1 << 21), dict(K=1 << 23), dict(M=1 << 30, N=1 << 20))
+BAD = (dict(M=-1), dict(N=-16), dict(K=-16), dict(N=24), dict(K=24), dict(G=0), dict(G=-3), dict(off=None),
+       dict(off=A + 2), dict(a=None), dict(a=A + 8), dict(b=None), dict(b=A + 8), dict(sa=None), dict(sa=A + 2),
+       dict(sb=None), dict(sb=A + 1))
+LARGE = (dict(G=1025), dict(M=1 << 31), dict(M=(1 << 31) - 256, N=16), dict(N=1 << 31), dict(N=1 << 21),
+         dict(K=1 << 23), dict(M=1 << 30, N=1 << 20))
 
 
 def refusals(f, bad, large=LARGE):
@@ -192,16 +194,22 @@ def test_every_form_is_tested():
 
 def test_limits_between_the_forms(form):
     for args, want in (
-            ((1, 1, 0, 1, 8192, 1024, 1), (16, 32, 0)), ((1, 1, 0, 1, 16400, 5104, 1), (16, 32, 0)), ((1, 1, 0, 1, 16400, 5120, 1), (16, 64, 0)), ((0, 1, 0, 1, 16400, 1024, 1), (16, 64, 0)),
-            ((1, 1, 0, 1, 16384, 1024, 1), (16, 64, 0)), ((1, 1, 0, 32, 16384, 1024, 1), (32, 64, 0)), ((1, 1, 0, 33, 16384, 1024, 1), (64, 64, 0)),
-            ((0, 1, 0, 33, 16384, 1024, 1), (32, 64, 0)), ((0, 1, 0, 41, 16384, 1024, 1), (0, 128, 2)), ((0, 0, 0, 64, 16384, 1024, 1), (32, 64, 0)),
-            ((0, 0, 0, 65, 16384, 1024, 1), (0, 128, 1)), ((0, 0, 0, 512, 2048, 1024, 1), (32, 64, 0)), ((0, 0, 0, 513, 2048, 1024, 1), (0, 128, 1)), ((1, 1, 0, 65, 16384, 1024, 1), (0, 128, 2)), ((1, 1, 1, 320, 16384, 1024, 16), (16, 32, 0)),
-            ((0, 1, 1, 320, 16384, 1024, 16), (16, 64, 0)), ((0, 1, 1, 640, 16384, 1024, 16), (32, 64, 0)), ((1, 1, 1, 640, 16384, 1024, 16), (0, 128, 1)),
-            ((0, 0, 1, 640, 16384, 1024, 16), (32, 64, 0)), ((0, 0, 1, 641, 16384, 1024, 16), (0, 128, 1)), ((1, 1, 0, 64, 4096, 1024, 1), (32, 32, 0)),
-            ((1, 1, 0, 128, 4096, 1024, 1), (32, 64, 0)), ((1, 1, 0, 256, 16384, 1024, 1), (0, 128, 2)), ((0, 0, 0, 256, 16384, 1024, 1), (0, 128, 1)),
-            ((0, 1, 1, 256, 1040, 1024, 4), (32, 64, 0)), ((1, 1, 0, 2048, 4096, 1024, 1), (0, 128, 1)), ((1, 1, 1, 2048, 4096, 1024, 8), (0, 256, 1)),
-            ((1, 1, 0, 1003, 4176, 1024, 1), (0, 128, 1)), ((1, 1, 1, 16640, 16384, 1024, 16), (0, 256, 1)),
-            ((1, 1, 0, 2147483391, 2097072, 1024, 1), (0, 256, 1)), ((1, 1, 1, 1, 16, 1024, 1024), (16, 32, 0))):
+            ((1, 1, 0, 1, 8192, 1024, 1), (16, 32, 0)), ((1, 1, 0, 1, 16400, 5104, 1), (16, 32, 0)),
+            ((1, 1, 0, 1, 16400, 5120, 1), (16, 64, 0)), ((0, 1, 0, 1, 16400, 1024, 1), (16, 64, 0)),
+            ((1, 1, 0, 1, 16384, 1024, 1), (16, 64, 0)), ((1, 1, 0, 32, 16384, 1024, 1), (32, 64, 0)),
+            ((1, 1, 0, 33, 16384, 1024, 1), (64, 64, 0)), ((0, 1, 0, 33, 16384, 1024, 1), (32, 64, 0)),
+            ((0, 1, 0, 41, 16384, 1024, 1), (0, 128, 2)), ((0, 0, 0, 64, 16384, 1024, 1), (32, 64, 0)),
+            ((0, 0, 0, 65, 16384, 1024, 1), (0, 128, 1)), ((0, 0, 0, 512, 2048, 1024, 1), (32, 64, 0)),
+            ((0, 0, 0, 513, 2048, 1024, 1), (0, 128, 1)), ((1, 1, 0, 65, 16384, 1024, 1), (0, 128, 2)),
+            ((1, 1, 1, 320, 16384, 1024, 16), (16, 32, 0)), ((0, 1, 1, 320, 16384, 1024, 16), (16, 64, 0)),
+            ((0, 1, 1, 640, 16384, 1024, 16), (32, 64, 0)), ((1, 1, 1, 640, 16384, 1024, 16), (0, 128, 1)),
+            ((0, 0, 1, 640, 16384, 1024, 16), (32, 64, 0)), ((0, 0, 1, 641, 16384, 1024, 16), (0, 128, 1)),
+            ((1, 1, 0, 64, 4096, 1024, 1), (32, 32, 0)), ((1, 1, 0, 128, 4096, 1024, 1), (32, 64, 0)),
+            ((1, 1, 0, 256, 16384, 1024, 1), (0, 128, 2)), ((0, 0, 0, 256, 16384, 1024, 1), (0, 128, 1)),
+            ((0, 1, 1, 256, 1040, 1024, 4), (32, 64, 0)), ((1, 1, 0, 2048, 4096, 1024, 1), (0, 128, 1)),
+            ((1, 1, 1, 2048, 4096, 1024, 8), (0, 256, 1)), ((1, 1, 0, 1003, 4176, 1024, 1), (0, 128, 1)),
+            ((1, 1, 1, 16640, 16384, 1024, 16), (0, 256, 1)), ((1, 1, 0, 2147483391, 2097072, 1024, 1), (0, 256, 1)),
+            ((1, 1, 1, 1, 16, 1024, 1024), (16, 32, 0))):
         assert form(*args, CUS) == want, args
 
 

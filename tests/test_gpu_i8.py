@@ -57,6 +57,18 @@ def test_cast_of_every_value_beside_a_maximum():
         assert_same_bytes(s.cpu().numpy(), want_s, hex(top))
 
 
+def test_cast_of_more_rows_than_a_launch_has_workgroups():
+    """2^24 rows and a few: workgroups walk on. Every row against the first ones, whose values it repeats."""
+    M, period = (1 << 24) + 37, 4099
+    x = torch.from_numpy(wl.randn_bf16(np.random.default_rng(5), (period, 8), 0.5, 0.01, 20.0).view(np.int16)).cuda()
+    rows = torch.arange(M, device="cuda") % period
+    q, s = feedforward.mgs_quant_rows_i8(x[rows])
+    want_q, want_s = ff.quant_rows_i8(x.cpu().numpy().view(np.uint16))
+    assert_same_bytes(q[:period].cpu().numpy(), want_q, "q")
+    assert_same_bytes(s[:period].cpu().numpy(), want_s, "scales")
+    assert torch.equal(q, q[:period][rows]) and torch.equal(s, s[:period][rows])
+
+
 def test_cast_of_weights():
     rng = np.random.default_rng(1)
     w = wl.randn_bf16(rng, (3, 48, 272), 0.02, 0.001, 0.5)

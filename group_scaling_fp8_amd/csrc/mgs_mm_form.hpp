@@ -72,7 +72,7 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 //   1000 rows by 800 x 8192: 34 with 64 and 64, 37 on tiles; gradient of 256 rows,
 //   2048 x 4096: E 18 with 32 and 64, 28 on tiles, X 19 and 43; E has no registers for
 //   64 and 64). X takes 32 and 64 for two rounds of them too (64 rows, 2 x 8192 x 5120:
-//   39, on tiles 50; three rounds 56).
+//   39, on tiles 43; three rounds 56).
 // - up to 20 rows a group 16 rows a tile, whatever the weights: with 64 lines, which read a
 //   row half as often (E, 4 tokens to 2 of 16 experts of 2 x 8192 x 5120: 116, with 32
 //   lines 134, on tiles 137; I: 111, 121 and 125), but with 32 for I of short rows, which
@@ -86,7 +86,8 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 //   4096 x 4096: 37 on tiles of 128 and 52; 2048 rows in 8 groups: 69 and 58; 4096
 //   rows in 16 groups, 4112 x 4176: 187 and 164).
 // - two sets of waves on a tile of 128 x 128 where there is one a CU at most (256 rows,
-//   2 x 8192 x 5120: 33, one set 39; with 264 tiles 52 and 37).
+//   2 x 8192 x 5120: 33, one set 39, X 49 and 55; 128 rows, X 44 and 51; with 264 tiles 52
+//   and 37).
 inline MmForm mm_form_rows(bool ints, bool eight, bool grouped, int64_t M, int64_t N, int64_t K, int64_t G, int cus) {
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     const int64_t groups = grouped ? G : 1, extra = grouped ? G / 2 : 0, rows = up(M, groups);
@@ -95,9 +96,10 @@ inline MmForm mm_form_rows(bool ints, bool eight, bool grouped, int64_t M, int64
         if ((up(M, kFew[i][0]) + extra) * up(N, kFew[i][1]) <= cus) return {kFew[i][0], kFew[i][1], 0};
     if (rows <= 20) return {16, ints && K < 5120 ? 32 : 64, 0};
     if (rows <= 40 && (groups == 1 || !ints)) return {32, 64, 0};
-    if (!eight) return (up(M, 32) + extra) * up(N, 64) <= 2 * cus ? MmForm{32, 64, 0} : MmForm{0, 128, 1};
+    if (!eight && (up(M, 32) + extra) * up(N, 64) <= 2 * cus) return {32, 64, 0};
     const int64_t large = (up(M, 256) + extra) * up(N, 256), small = (up(M, 128) + extra) * up(N, 128);
     if (small <= cus) return {0, 128, 2};
+    if (!eight) return {0, 128, 1};
     const int64_t left = small % (2 * cus);
     const int64_t small_time = small / (2 * cus) * 100 + (left == 0 ? 0 : left <= cus ? 65 : 100);
     return {0, up(large, cus) * 147 < small_time ? 256 : 128, 1};

@@ -1351,6 +1351,8 @@ hipError_t launch_sized(const MmArgs& p, int cus, hipStream_t stream) {
     if (form.few == 32) return launch_few<32, 32, Few>(p, cus, stream);
     if constexpr (KIND::wgrad || KIND::eight) {
         if (form.tile == 256) return launch<256, 256, 128, 64, 1, KIND>(p, cus, stream);
+    }
+    if constexpr (KIND::wgrad || KIND::eight || KIND::halves) {
         if (form.sets == 2) return launch<128, 128, 64, 64, 2, KIND>(p, cus, stream);
     }
     return launch<128, 128, 64, 64, 1, KIND>(p, cus, stream);

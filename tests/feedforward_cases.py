@@ -26,7 +26,7 @@ ROWS = [
     (900, 144, 144, 6, "bad", FEW32_32, FEW32_32, FEW32_32),
     (30, 4064, 1040, 1, "even", FEW16_32, FEW16_32, FEW16_32),
     (250, 960, 272, 1, "none", FEW32_32, FEW32_32, FEW32_32),
-    (1500, 1200, 144, 1, "none", TWO128, TWO128, TILE128),
+    (1500, 1200, 144, 1, "none", TWO128, TWO128, TWO128),
     (1000, 160, 400, 9, "bad", FEW32_32, FEW32_32, FEW32_32),
     (30, 8192, 144, 1, "none", FEW32_32, FEW32_32, FEW32_32),
     (250, 960, 272, 4, "tail", FEW32_64, FEW32_64, FEW32_64),
@@ -44,10 +44,10 @@ ROWS = [
     (1000, 800, 272, 1, "none", FEW64_64, TWO128, FEW32_64),
     (1200, 544, 144, 9, "tail", FEW64_64, TWO128, FEW32_64),
     (700, 1200, 656, 1, "none", FEW64_64, TWO128, FEW32_64),
-    (2000, 1200, 528, 5, "tail", TWO128, TWO128, TILE128),
-    (1500, 1200, 16, 4, "one", TWO128, TWO128, TILE128),
-    (1500, 1200, 272, 4, "empty", TWO128, TWO128, TILE128),
-    (2000, 1200, 144, 5, "bad", TWO128, TWO128, TILE128),
+    (2000, 1200, 528, 5, "tail", TWO128, TWO128, TWO128),
+    (1500, 1200, 16, 4, "one", TWO128, TWO128, TWO128),
+    (1500, 1200, 272, 4, "empty", TWO128, TWO128, TWO128),
+    (2000, 1200, 144, 5, "bad", TWO128, TWO128, TWO128),
     (1003, 4192, 272, 1, "none", TILE128, TILE128, TILE128),
     (2000, 2336, 528, 5, "even", TILE128, TILE128, TILE128),
     (2000, 2336, 400, 5, "bad", TILE128, TILE128, TILE128),

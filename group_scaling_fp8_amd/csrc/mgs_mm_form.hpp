@@ -70,8 +70,8 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 //   most: its eight waves share a contraction however few tiles there are (I, 64 rows by
 //   4096 x 4096: 11.6 with 32 rows and 32 lines, 14.6 with 16, 20.5 on tiles of 128 x 128;
 //   1000 rows by 800 x 8192: 34 with 64 and 64, 37 on tiles; gradient of 256 rows,
-//   2048 x 4096: E 18 with 32 and 64, 28 on tiles, X 19 and 43; E has no registers for
-//   64 and 64). X takes 32 and 64 for two rounds of them too (64 rows, 2 x 8192 x 5120:
+//   2048 x 4096: E 18 with 32 and 64, 28 on tiles, X 19 and, with one set of waves, 43; E
+//   has no registers for 64 and 64). X takes 32 and 64 for two rounds of them too (64 rows, 2 x 8192 x 5120:
 //   39, on tiles 43; three rounds 56).
 // - up to 20 rows a group 16 rows a tile, whatever the weights: with 64 lines, which read a
 //   row half as often (E, 4 tokens to 2 of 16 experts of 2 x 8192 x 5120: 116, with 32

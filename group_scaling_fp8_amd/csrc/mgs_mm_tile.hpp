@@ -987,17 +987,22 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
 constexpr int kFewWaves = 8;
 
 // The 16 bytes at p + at and those at APART bytes from them, of a row of len bytes
-// (a multiple of 16, not 0); zeros past its end.
+// (a multiple of 16, not 0); past its end its first bytes, which within() clears.
 template <int APART>
 __device__ __forceinline__ v8i load32(const uint8_t* p, int64_t at, int64_t len) {
-    const bool first = at < len, second = at + APART < len;
-    const v4i lo = *reinterpret_cast<const v4i*>(p + (first ? at : 0));
-    const v4i hi = *reinterpret_cast<const v4i*>(p + (second ? at + APART : 0));
-    const v4i zero = {};
-    return __builtin_shufflevector(first ? lo : zero, second ? hi : zero, 0, 1, 2, 3, 4, 5, 6, 7);
+    const v4i lo = *reinterpret_cast<const v4i*>(p + (at < len ? at : 0));
+    const v4i hi = *reinterpret_cast<const v4i*>(p + (at + APART < len ? at + APART : 0));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int BM, int LINES, int DEPTH, class KIND>
+template <int APART>
+__device__ __forceinline__ v8i within(v8i v, int64_t at, int64_t len) {
+    const v4i zero = {};
+    const v4i lo = __builtin_shufflevector(v, v, 0, 1, 2, 3), hi = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+    return __builtin_shufflevector(at < len ? lo : zero, at + APART < len ? hi : zero, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <int BM, int LINES, int DEPTH, bool WALKS, class KIND>
 __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
     constexpr bool WGRAD = KIND::wgrad, GATED = KIND::gated, GRAD = KIND::grad, F32 = KIND::f32;
     constexpr bool SCALED = KIND::scaled, INT8 = KIND::num == Num::Int8;
@@ -1095,9 +1100,22 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
         v8i a[MT], b[NT];
         float sa[MT], sb[BLOCKS];
     };
+    constexpr int APART = KIND::halves ? 64 : 16;
+    // What lies past the rows' end is cleared where a block is multiplied: behind its
+    // loads the selects wait for them, before the block at hand is multiplied (one row by
+    // 8192 x 8192 12.9 us, so 14.2; wgrad of 4 x 512 x 512 31, 33; gradient of one row,
+    // 8192 x 5120, 9.9 and 11.1). Sixteen rows of a gated pair do wait there: tiles in
+    // turn read two weights each, and lose with more of their loads under way (four tokens
+    // to 2 of 16 experts, 2 x 8192 x 5120, 118 us, without the wait 124; integers, to 8 of
+    // 64 of 2 x 2048 x 4096, 85 and 87).
+    constexpr bool WAITS = GATED && BM == 16;
+    auto place = [&](int k) { return (int64_t)k * kBK + fg * (KIND::halves ? 16 : 32); };
     auto fetch = [&](Block& x, int k) {
-        const int64_t at = (int64_t)k * kBK + fg * (KIND::halves ? 16 : 32);
-        auto get = [&](const uint8_t* q) { return load32<KIND::halves ? 64 : 16>(q, at, len); };
+        const int64_t at = place(k);
+        auto get = [&](const uint8_t* q) {
+            const v8i v = load32<APART>(q, at, len);
+            return WAITS ? within<APART>(v, at, len) : v;
+        };
 #pragma unroll
         for (int j = 0; j < NT; ++j) x.b[j] = get(pb[j]);
 #pragma unroll
@@ -1110,7 +1128,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
             for (int w = 0; w < BLOCKS; ++w) x.sb[w] = psb[w][k];
     };
     Acc acc[MT][NT];
-    auto multiply = [&](const Block& x) {
+    auto multiply = [&](Block& x, int k) {
+        if (!WAITS && (int64_t)(k + 1) * kBK > len) {          // the rows end in this block
+#pragma unroll
+            for (int j = 0; j < NT; ++j) x.b[j] = within<APART>(x.b[j], place(k), len);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) x.a[i] = within<APART>(x.a[i], place(k), len);
+        }
         float f[MT][BLOCKS];
         if constexpr (SCALED)
 #pragma unroll
@@ -1204,17 +1228,20 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
         for (int d = 0; d < DEPTH; ++d) {
             const int now = k + d * kFewWaves;
             if (now >= nkb) break;
-            const Block y = x[d];
+            Block y = x[d];
             if (now + DEPTH * kFewWaves < nkb) fetch(x[d], now + DEPTH * kFewWaves);
-            multiply(y);
+            multiply(y, now);
         }
     }
     // the next tile's first loads are on their way while this one is joined
-    wg += grid;
-    const bool more = wg < total;
-    if (more) {
-        t = locate((int)wg);
-        begin(t);
+    bool more = false;
+    if constexpr (WALKS) {
+        wg += grid;
+        more = wg < total;
+        if (more) {
+            t = locate((int)wg);
+            begin(t);
+        }
     }
 
     // ---- join and store ----
@@ -1310,7 +1337,18 @@ hipError_t launch_few(const MmArgs& p, int cus, hipStream_t stream) {
     constexpr int DEPTH = KIND::num == Num::Int8 && BM == 16 && LINES == 64 ? 2 : 1;
     const int64_t most = cus * (BM == 16 && LINES == 32 ? 16 : 8) / kFewWaves;       // by registers
     const int64_t blocks = WGRAD || tiles < most ? tiles : most;
-    hipLaunchKernelGGL((mm_few_kernel<BM, LINES, DEPTH, KIND>), grid_xz(blocks), dim3(kFewWaves * 64), 0, stream, p);
+    // block128 and wgrad without the code that walks, which costs 0.3 us a call (one row by
+    // 1024 x 1024: 4.7, without it 4.4).
+    if constexpr (WGRAD || !KIND::halves) {
+        if (blocks == tiles) {
+            hipLaunchKernelGGL((mm_few_kernel<BM, LINES, DEPTH, false, KIND>), grid_xz(blocks), dim3(kFewWaves * 64), 0,
+                               stream, p);
+            return hipGetLastError();
+        }
+    }
+    if constexpr (!WGRAD)
+        hipLaunchKernelGGL((mm_few_kernel<BM, LINES, DEPTH, true, KIND>), grid_xz(blocks), dim3(kFewWaves * 64), 0, stream,
+                           p);
     return hipGetLastError();
 }
 

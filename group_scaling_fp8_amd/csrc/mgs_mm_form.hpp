@@ -1,4 +1,5 @@
-// mgs_mm_form.hpp — which form a product takes (internal; host only, no HIP).
+// mgs_mm_form.hpp — which form a product takes, and how many tiles rows take
+// (internal; no HIP).
 #pragma once
 
 #include <stdint.h>
@@ -6,6 +7,10 @@
 namespace mgs {
 
 constexpr int kFewCols = 32;      // columns of a tile of the form for few rows
+
+// Tiles of `high` rows that hold `rows` rows, of which there are up to 2^31 - 1: the sum
+// passes 31 bits.
+constexpr int tiles_down(int rows, int high) { return (int)(((uint32_t)rows + (uint32_t)high - 1) / (uint32_t)high); }
 
 struct MmForm {
     int few;      // rows of a tile of the form for few rows or few outputs, or 0:

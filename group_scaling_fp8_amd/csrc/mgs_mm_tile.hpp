@@ -290,7 +290,7 @@ struct Groups {
             const int e = max(wave_prefix_imax(raw), carry);
             int b = __shfl_up(e, 1, kWave);
             if (lane == 0) b = carry;
-            const int u = tiles + wave_prefix_sum((e - b + rows - 1) / rows);
+            const int u = tiles + wave_prefix_sum(tiles_down(e - b, rows));
             if (g < G) {
                 end[g] = e;
                 upto[g] = u;
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
         total = p.G * row_tiles * col_tiles;
     } else {
         // the rows past the last group are one more group whose tiles are zeros
-        total = (uniform(s_groups.upto[p.G - 1]) + ((int)p.M - end_of(p.G - 1) + BM - 1) / BM) * col_tiles;
+        total = (uniform(s_groups.upto[p.G - 1]) + tiles_down((int)p.M - end_of(p.G - 1), BM)) * col_tiles;
     }
     auto tile = [&](int b) {
         const int L = tile_of(b, total);
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64 * PARTS, 2) void mm_kernel
             const int last = t.g < 0 ? p.G - 1 : t.g - 1;      // the group before
             const int begin = end_of(last), end = t.g < 0 ? (int)p.M : end_of(t.g);
             const int first = last < 0 ? 0 : uniform(s_groups.upto[last]);
-            patch(L - first * col_tiles, (end - begin + BM - 1) / BM, col_tiles, row, col);
+            patch(L - first * col_tiles, tiles_down(end - begin, BM), col_tiles, row, col);
             t.m0 = begin + uniform(row) * BM;
             t.n0 = uniform(col) * COLS;
             t.row_end = end;
@@ -1025,7 +1025,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
         e = max(wave_prefix_imax(raw), from);
         b = __shfl_up(e, 1, kWave);
         if (lane == 0) b = from;
-        upto = before + wave_prefix_sum((e - b + BM - 1) / BM);
+        upto = before + wave_prefix_sum(tiles_down(e - b, BM));
     };
     const int row_tiles = (int)((p.N + BM - 1) / BM);                  // wgrad: down one matrix
     int last_end = 0, tiles = 0, total;
@@ -1037,7 +1037,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
             tiles = uniform(__shfl(upto, kWave - 1, kWave));
             last_end = uniform(__shfl(e, kWave - 1, kWave));
         }
-        total = (tiles + (M - last_end + BM - 1) / BM) * col_tiles;    // the rows past the last group give zeros
+        total = (tiles + tiles_down(M - last_end, BM)) * col_tiles;    // the rows past the last group give zeros
     }
     struct FewTile {
         int g, begin, end;                 // the group (-1: none) and its rows, wgrad: its part of the contraction
@@ -1078,9 +1078,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
             t.g = uniform(base + at);
             t.begin = uniform(__shfl(b, at, kWave));
             t.end = uniform(__shfl(e, at, kWave));
-            before = uniform(__shfl(upto, at, kWave)) - (t.end - t.begin + BM - 1) / BM;
+            before = uniform(__shfl(upto, at, kWave)) - tiles_down(t.end - t.begin, BM);
         }
-        const int rows = (t.end - t.begin + BM - 1) / BM, local = L - before * col_tiles;
+        const int rows = tiles_down(t.end - t.begin, BM), local = L - before * col_tiles;
         t.m0 = t.begin + local % rows * BM;
         t.n0 = local / rows * COLS;
         return t;

@@ -428,7 +428,7 @@ int mgs_quant_blocks128(const void *w, int64_t E, int64_t N, int64_t K, uint32_t
  *   out_type     MGS_OUT_BF16 or MGS_OUT_F32.
  *   y            (M, N), written.
  * The scales are finite and positive. A row's result does not depend on other
- * rows. Requirements: N % 16 == 0, K % 16 == 0, K < 2^23 - 256,
+ * rows. Requirements: M < 2^31, N % 16 == 0, K % 16 == 0, K < 2^23 - 256,
  * N < 2^21 - 64, n_groups <= MGS_MAX_GROUPS; a, b and y 16-byte aligned. K == 0 gives zeros.
  */
 int mgs_mm_block128(const void *a, const float *a_scales, int64_t M, int64_t K, const void *b, const float *b_scales,

@@ -32,6 +32,7 @@ from .api import _BF16_LIKE, _U8_LIKE, _need, _out, _stream_handle
 from .experts import _input, _out_type, _ptr
 
 _I8, _F32, _I32 = (torch.int8,), (torch.float32,), (torch.int32,)
+_ZEROS_SCALE = 127000001904640.0            # 127 / 1e-12 in float32, the scale of a row of zeros
 
 
 def _run(name: str, t: torch.Tensor, *args):
@@ -42,6 +43,13 @@ def _run(name: str, t: torch.Tensor, *args):
         with torch.cuda.device(t.device):
             st = getattr(lib(), name)(*args)
     check(name, st)
+
+
+def _stream(stream, device):
+    """`stream`, or the device's current one, as torch's own object."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream), device=device)
 
 
 def _given(t, first, name: str, dtypes, shape):
@@ -126,7 +134,8 @@ def mgs_quant_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scales:
                       stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """8-bit integers with one scale for each row: x (M, K) bf16, or the
     weights (E, N, K) of experts. Returns q int8 of x's shape and scales
-    float32 of its leading dims."""
+    float32 of its leading dims; rows of no columns have the scale of rows of
+    zeros."""
     _need(x, "x", _BF16_LIKE)
     if x.dim() not in (2, 3):
         raise ValueError("x must have 2 or 3 dims")
@@ -135,6 +144,10 @@ def mgs_quant_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scales:
     else:
         q = _out(q, tuple(x.shape), torch.int8, x.device, "q", stream)
         scales = _out(scales, tuple(x.shape[:-1]), torch.float32, x.device, "scales", stream)
+    if x.shape[-1] == 0:                                     # the call does nothing
+        with torch.cuda.device(x.device), torch.cuda.stream(_stream(stream, x.device)):
+            scales.fill_(_ZEROS_SCALE)
+        return q, scales
     _run("mgs_quant_rows_i8", x, x.data_ptr(), scales.numel(), x.shape[-1], q.data_ptr(), scales.data_ptr(),
          _stream_handle(stream, x))
     return q, scales

@@ -531,7 +531,7 @@ int mgs_mm_gated_grad_block128(const void *dy, const float *dy_scales, int64_t M
  * max(amax, 1e-12)), q (M, K) int8 = fl32(x * scale) rounded to the nearest
  * integer, ties to even: -127 to 127. x is finite. The weights of E experts
  * (E, N, K) are E * N rows. Requirements: M and K < 2^31, K % 8 == 0; x 16-byte
- * aligned, q 8-byte aligned. M == 0 or K == 0 is a no-op.
+ * aligned, q 8-byte aligned. M == 0 or K == 0 is a no-op, which writes no scales.
  */
 int mgs_quant_rows_i8(const void *x, int64_t M, int64_t K, void *q, float *scales, void *stream);
 

@@ -91,7 +91,9 @@ __global__ __launch_bounds__(kThreads<LANES>) void rows_i8_kernel(const uint16_t
             for (int j = 0; j < V; ++j) m = mag_max8(m, v[j]);
             if (HELD || c0 + LANES * V * 8 >= K) break;
         }
-        const float s = 127.0f / fmaxf(__uint_as_float(row_max<LANES>(mag_fold(m), s_max) << 16), 1e-12f);
+        // the largest magnitude as bits is a NaN's if the row holds one, and the scale then NaN
+        const float amax = __uint_as_float(row_max<LANES>(mag_fold(m), s_max) << 16);
+        const float s = 127.0f / (amax < 1e-12f ? 1e-12f : amax);
         if (mine && lane == 0) scales[r] = s;
         for (int64_t c0 = 0; c0 < K; c0 += LANES * V * 8) {
 #pragma unroll

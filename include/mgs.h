@@ -529,8 +529,9 @@ int mgs_mm_gated_grad_block128(const void *dy, const float *dy_scales, int64_t M
 /*
  * One scale for each row: x (M, K) bf16, scales (M) fp32 = fl32(127 /
  * max(amax, 1e-12)), q (M, K) int8 = fl32(x * scale) rounded to the nearest
- * integer, ties to even: -127 to 127. x is finite. The weights of E experts
- * (E, N, K) are E * N rows. Requirements: M and K < 2^31, K % 8 == 0; x 16-byte
+ * integer, ties to even: -127 to 127. A row that holds a NaN or an infinity
+ * has zeros and the scale NaN or 0, which make its products NaN. The weights of
+ * E experts (E, N, K) are E * N rows. Requirements: M and K < 2^31, K % 8 == 0; x 16-byte
  * aligned, q 8-byte aligned. M == 0 or K == 0 is a no-op, which writes no scales.
  */
 int mgs_quant_rows_i8(const void *x, int64_t M, int64_t K, void *q, float *scales, void *stream);
@@ -543,8 +544,9 @@ int mgs_quant_rows_i8(const void *x, int64_t M, int64_t K, void *q, float *scale
  *   b, b_scales  (n_groups, N, K) int8, (n_groups, N) fp32.
  *   offsets, out_type, y  as for mgs_mm_block128. Rows past the last end give
  *                zeros.
- * The scales are finite and positive. Requirements: M < 2^31 - 256, N % 16 == 0,
- * K % 16 == 0, K <= MGS_I8_MAX_K, N < 2^21 - 64, n_groups <= MGS_MAX_GROUPS; a, b
+ * The scales are finite and positive; one that mgs_quant_rows_i8 gave a row that
+ * is not finite makes that row or column NaN. Requirements: M < 2^31 - 256,
+ * N % 16 == 0, K % 16 == 0, K <= MGS_I8_MAX_K, N < 2^21 - 64, n_groups <= MGS_MAX_GROUPS; a, b
  * and y 16-byte aligned. K == 0 gives zeros.
  */
 int mgs_mm_i8(const void *a, const float *a_scales, int64_t M, int64_t K, const void *b, const float *b_scales,

@@ -80,9 +80,15 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 //   39, on tiles 43; three rounds 56).
 // - up to 20 rows a group 16 rows a tile, whatever the weights: with 64 lines, which read a
 //   row half as often (E, 4 tokens to 2 of 16 experts of 2 x 8192 x 5120: 116, with 32
-//   lines 134, on tiles 137; I: 111, 121 and 125), but with 32 for I of short rows, which
-//   have too few blocks a wave (16 tokens to 4 of 64 experts of 2 x 2048 x 4096: 99, with
-//   64 lines 110; E 111 and 110).
+//   lines 134, on tiles 137; 16 tokens to 4 of 64 of 2 x 2048 x 4096: 110 and 111). I
+//   takes 64 lines only where every wave has enough blocks to run two ahead, three and a
+//   half of them where workgroups walk eight tiles and five where they walk fewer (32 lines
+//   | 64; 4 tokens to 2 of 16, 2 x 8192 columns, by the contraction: 2560 68 | 70, 3584 90 |
+//   89, 4608 112 | 111, 5632 135 | 130, 7168 166 | 161; 16 to 4 of 64, one product of 4096:
+//   2560 77 | 78, 3584 99 | 98, 4608 125 | 120, 7168 185 | 178; 16 to 2 of 16, 2 x 2048: 3584
+//   48 | 49, 4608 59 | 60, 5632 66 | 67; 16 rows by 32768: 4608 34 | 30, 5632 44 | 40). Rows of
+//   a multiple of 4096 bytes, of which 64 lines begin on the same channels, take 32
+//   whatever their length (4096: 99 | 108, 99 | 105, 111 | 113; 8192: 188 | 195, 94 | 103).
 // - up to 40 rows 32 and 64, for I only where there is one group (E, 64 tokens to 8 of 64
 //   experts of 2 x 2048 x 4096: 218, on tiles 234; I, more tokens a group: 277 and 269).
 // - tiles of 256 x 256, one a CU, or 128 x 128, two a CU: by the time of their
@@ -99,7 +105,11 @@ inline MmForm mm_form_rows(bool ints, bool eight, bool grouped, int64_t M, int64
     constexpr int kFew[5][2] = {{16, 32}, {32, 32}, {16, 64}, {32, 64}, {64, 64}};
     for (int i = 0; i < (ints ? 5 : 4); ++i)
         if ((up(M, kFew[i][0]) + extra) * up(N, kFew[i][1]) <= cus) return {kFew[i][0], kFew[i][1], 0};
-    if (rows <= 20) return {16, ints && K < 5120 ? 32 : 64, 0};
+    if (rows <= 20) {
+        const bool walks = (up(M, 16) + extra) * up(N, 64) >= 8 * cus;
+        const bool longer = K / 128 >= (walks ? 28 : 40) && K % 4096 != 0;
+        return {16, ints && !longer ? 32 : 64, 0};
+    }
     if (rows <= 40 && (groups == 1 || !ints)) return {32, 64, 0};
     if (!eight && (up(M, 32) + extra) * up(N, 64) <= 2 * cus) return {32, 64, 0};
     const int64_t large = (up(M, 256) + extra) * up(N, 256), small = (up(M, 128) + extra) * up(N, 128);

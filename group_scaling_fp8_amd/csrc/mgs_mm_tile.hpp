@@ -1006,8 +1006,13 @@ __device__ __forceinline__ v8i within(v8i v, int64_t at, int64_t len) {
     return __builtin_shufflevector(at < len ? lo : zero, at + APART < len ? hi : zero, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// Workgroups of eight waves that a CU holds at a time: two of at most 128 registers a lane,
+// which the smallest tiles need no more than (the gradient with binary32 sums 130).
+template <int BM, int LINES, class KIND>
+constexpr int kFewPerCu = BM == 16 && LINES == 32 && !(KIND::grad && !KIND::eight) ? 2 : 1;
+
 template <int BM, int LINES, int DEPTH, bool WALKS, class KIND>
-__global__ __launch_bounds__(kFewWaves * 64) void mm_few_kernel(MmArgs p) {
+__global__ __launch_bounds__(kFewWaves * 64, (kFewPerCu<BM, LINES, KIND> * kFewWaves / 4)) void mm_few_kernel(MmArgs p) {
     constexpr bool WGRAD = KIND::wgrad, GATED = KIND::gated, GRAD = KIND::grad, F32 = KIND::f32;
     constexpr bool SCALED = KIND::scaled, INT8 = KIND::num == Num::Int8;
     constexpr int MT = BM / 16, NT = LINES / 16;
@@ -1339,7 +1344,7 @@ hipError_t launch_few(const MmArgs& p, int cus, hipStream_t stream) {
     // Two blocks ahead pay for integers only, which have the registers (4 tokens to 2 of
     // 16 experts, 2 x 8192 x 5120: 140 to 117 us at the time; E4M3 116 to 125).
     constexpr int DEPTH = KIND::num == Num::Int8 && BM == 16 && LINES == 64 ? 2 : 1;
-    const int64_t most = cus * (BM == 16 && LINES == 32 ? 16 : 8) / kFewWaves;       // by registers
+    const int64_t most = cus * kFewPerCu<BM, LINES, KIND>;
     const int64_t blocks = WGRAD || tiles < most ? tiles : most;
     // block128 and wgrad without the code that walks, which costs 0.3 us a call (one row by
     // 1024 x 1024: 4.7, without it 4.4).

@@ -5,7 +5,8 @@ and only marshal arguments: they check torch tensors, allocate outputs the
 caller did not pass, and call the library on the current HIP stream. Every
 step of the computation runs in the library's HIP kernels. There is no CPU
 fallback: if libmgs.so is missing, the first call raises. The calls of gated
-feed-forward layers and of 8-bit integers are in the module ``feedforward``.
+feed-forward layers and of 8-bit integers stand in the module ``feedforward``
+and are found here by their names too.
 """
 from __future__ import annotations
 
@@ -23,4 +24,16 @@ from .experts import (  # noqa: F401
     mgs_mm_block128, mgs_mm_wgrad, mgs_moe_combine, mgs_moe_combine_grad, mgs_moe_dispatch, mgs_moe_rows,
     mgs_moe_sort, mgs_quant_blocks128, mgs_quant_rows128,
 )
-from . import feedforward  # noqa: E402,F401  (the gated feed-forward and 8-bit integer calls)
+from . import feedforward  # noqa: E402,F401
+
+_FEEDFORWARD = ("mgs_mm_gated_block128", "mgs_mm_gated_grad_block128", "mgs_quant_rows_i8", "mgs_mm_i8", "mgs_mm_gated_i8")
+
+
+def __getattr__(name):
+    if name in _FEEDFORWARD:
+        return getattr(feedforward, name)
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
+
+
+def __dir__():
+    return sorted([*globals(), *_FEEDFORWARD])

@@ -538,8 +538,10 @@ int mgs_quant_rows_i8(const void *x, int64_t M, int64_t K, void *q, float *scale
 
 /*
  * For m in group e: y[m, n] = sum_k a[m, k] * b[e, n, k] / (a_scales[m] *
- * b_scales[e, n]); the sum is exact and rounded to fp32 before it is divided by
- * a_scales[m], which fp32 has to hold, and then by b_scales[e, n].
+ * b_scales[e, n]). The sum is exact and rounded to fp32, multiplied by
+ * fl32(1 / a_scales[m]), which fp32 has to hold, and then by
+ * fl32(1 / b_scales[e, n]): five roundings of 2^-24 at most, and the output
+ * type's.
  *   a, a_scales  (M, K) int8, (M) fp32.
  *   b, b_scales  (n_groups, N, K) int8, (n_groups, N) fp32.
  *   offsets, out_type, y  as for mgs_mm_block128. Rows past the last end give

@@ -465,7 +465,10 @@ int mgs_mm_wgrad(const void *a_t, const float *a_scales_t, const void *b_t, cons
  * (n_groups, 2 F, K).
  *
  * act(g) = g * sigmoid(t(g)): MGS_ACT_SILU t = g, MGS_ACT_GELU the form with a
- * hyperbolic tangent, t = 2 sqrt(2 / pi) (g + 0.044715 g^3).
+ * hyperbolic tangent, t = 2 sqrt(2 / pi) (g + 0.044715 g^3). Projections that
+ * are infinite or NaN give what the formulas give: act(-inf) = -inf * 0 and
+ * act'(inf) = 1 + inf * 0 are NaN, act(inf) is inf. They reach no other column
+ * and no other row.
  */
 enum { MGS_ACT_SILU = 0, MGS_ACT_GELU = 1 };
 

@@ -19,6 +19,16 @@ def test_forms(form, case, gated):  # noqa: F811
         assert form(*args, kind != "none", M, N, K, G, CUS) == want
 
 
+def test_forms_of_the_range_tests(form):  # noqa: F811
+    """tests/test_gpu_activation_range.py: few rows, then each form of tiles, in a pair and in its gradient of twice the rows."""
+    import test_gpu_activation_range as rt
+    for rows, columns in ((rt.ROWS, 2 * rt.F), ([2 * m for m in rt.ROWS], rt.F)):
+        fast = [form(0, 1, 0, m, columns, 128, 1, CUS) for m in rows]
+        exact = [form(0, 0, 0, m, columns, 128, 1, CUS) for m in rows]
+        assert fast[0][0] and exact[0][0] and fast[1:] == [TWO128, TILE128, TILE256], (fast, exact)
+        assert exact[1:] == [TWO128, TILE128, TILE128], exact
+
+
 def test_every_form_of_tiles_runs_long():
     for tile in (TWO128, TILE128, TILE256):
         assert max(-(-c[2] // (128 * tile[2])) for c in LONG if tile in c[5:]) > MIN_STEPS + 4, tile

@@ -24,9 +24,12 @@ struct Activation {
     static constexpr float kFar = 8192.0f;
 
 #ifdef __HIP_DEVICE_COMPILE__
-    // exp2's argument is off by half a step, so the sigmoid's relative error is
-    // about 2^-24 |t| where it is small and 2^-22 elsewhere: far below a bf16's
-    // half step of 2^-9, down to where the result is below the normal numbers.
+    // exp2's argument takes four roundings in gelu (the coefficients, g^2, the fma, the
+    // product) and two in silu, each 2^-24 of it: e^-t is off by (4 |t| + 2) 2^-24 of
+    // itself, silu's by (2 |t| + 2) 2^-24, the sigmoid s by 1 - s of that and four more
+    // 2^-24 of the sum and the reciprocal. That is far below a bf16's half step of 2^-8.
+    // From t = -87 on, where s is below the normal numbers, it may be zero, also where
+    // g s u would be a normal number again.
     __device__ __forceinline__ float sigmoid(float g, float g2) const {
         return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * fmaf(e3, g2, e1)));
     }

@@ -15,7 +15,7 @@
 // 2623 TOP/s (16384^3; the library's at 2391), the gated pair at 2586 (16384 x 2 x
 // 8192 x 8192), bound by the matrix cores; in 16 ragged groups (16640 rows, 2 x 8192
 // x 5120) 1335 us, of which the rows of tiles past a group's end are 12%. One row by
-// 8192 x 8192 13.1 us, bound by the weights' bytes at 5.1 TB/s. Rows whose length is no
+// 8192 x 8192 12.5 us, bound by the weights' bytes at 5.4 TB/s. Rows whose length is no
 // multiple of 128 cross a line in every step: 4096 rows in 16 groups by 4096 x 4176
 // take 164 us, by 4096 x 4096 126.
 #include "mgs_experts.hpp"

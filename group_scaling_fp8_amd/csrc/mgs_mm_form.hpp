@@ -20,16 +20,16 @@ struct MmForm {
 
 // Which form a product takes, from the sizes the host knows (us, MI355X):
 // - few rows: up to 20 rows a group on average, one row of fragments (M = 1 by
-//   8192 x 8192: 17, against 66 on tiles of 128 x 128; more rows a group only
-//   where there is one group: 512 rows in 16 groups by 2048 x 4096 take 58, and
-//   33 on tiles); up to 40 rows two, and four where that is at most one
-//   workgroup a CU (64 rows by 8192 x 8192: 39 and 66; 256 rows by 4096 x 4096,
-//   two a CU: 36 and 32).
+//   8192 x 8192: 13, against 50 on tiles of 128 x 128; more rows a group only
+//   where there is one group: 512 rows in 16 groups by 2048 x 4096 take 51, and
+//   39 on tiles); up to 40 rows two, and four where that is at most one
+//   workgroup a CU (64 rows by 8192 x 8192: 33 and 40; 256 rows by 4096 x 4096,
+//   two a CU: 35 and 24).
 // - few outputs of wgrad: the same form with the fewest rows a tile that still
-//   leaves one workgroup a CU (16640 x 256 x 272: 25 with 16 rows, 48 with 64, and
+//   leaves one workgroup a CU (16640 x 256 x 272: 25 with 16 rows, 47 with 64, and
 //   66 on tiles of 128 x 128 in two parts; 16384 x 1024 x 512: 48 and 60, twice as
-//   many outputs 93 and 61; with binary32 sums still 93 and 94, and 43 and 52 in
-//   four groups of 512 x 512).
+//   many outputs 92 and 61; with binary32 sums 92 and 95, and 32 and 52 in four
+//   groups of 512 x 512).
 // - 256 x 256 tiles where they fill the CUs, twice if groups end inside them
 //   (block128 16640 x 5120 x 8192 in 16 groups: 780, and about 1000 with 128 x
 //   128; 2048 x 4096 x 4096, half the CUs: 66 and 48) and, for wgrad, where the
@@ -73,14 +73,14 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 // for each. (us, MI355X; I: integers, E: E4M3, X: E4M3 with binary32 sums.)
 // - the form for few rows with the smallest tile that leaves one workgroup a CU at
 //   most: its eight waves share a contraction however few tiles there are (I, 64 rows by
-//   4096 x 4096: 11.6 with 32 rows and 32 lines, 14.6 with 16, 20.5 on tiles of 128 x 128;
-//   1000 rows by 800 x 8192: 34 with 64 and 64, 37 on tiles; gradient of 256 rows,
-//   2048 x 4096: E 18 with 32 and 64, 28 on tiles, X 19 and, with one set of waves, 43; E
-//   has no registers for 64 and 64). X takes 32 and 64 for two rounds of them too (64 rows, 2 x 8192 x 5120:
-//   39, on tiles 43; three rounds 56).
+//   4096 x 4096: 10.9 with 32 rows and 32 lines, 14.4 with 16, 20.6 on tiles of 128 x 128;
+//   1000 rows by 800 x 8192: 33 with 64 and 64, 36 on tiles; gradient of 256 rows,
+//   2048 x 4096: E 17 with 32 and 64, 28 on tiles, X 18 and 39; E has no registers for 64
+//   and 64). X takes 32 and 64 for two rounds of them too (64 rows, 2 x 8192 x 5120: 38, on
+//   tiles 43; three rounds, 96 rows, 55 and 43).
 // - up to 20 rows a group 16 rows a tile, whatever the weights: with 64 lines, which read a
-//   row half as often (E, 4 tokens to 2 of 16 experts of 2 x 8192 x 5120: 116, with 32
-//   lines 134, on tiles 137; 16 tokens to 4 of 64 of 2 x 2048 x 4096: 110 and 111). I
+//   row half as often (E, 4 tokens to 2 of 16 experts of 2 x 8192 x 5120: 118, with 32
+//   lines 137, on tiles 138; 16 tokens to 4 of 64 of 2 x 2048 x 4096: 109, 111, 115). I
 //   takes 64 lines only where every wave has enough blocks to run two ahead, three and a
 //   half of them where workgroups walk eight tiles and five where they walk fewer (32 lines
 //   | 64; 4 tokens to 2 of 16, 2 x 8192 columns, by the contraction: 2560 68 | 70, 3584 90 |
@@ -89,8 +89,10 @@ inline MmForm mm_form(bool wgrad, bool fast, bool grouped, int64_t M, int64_t N,
 //   48 | 49, 4608 59 | 60, 5632 66 | 67; 16 rows by 32768: 4608 34 | 30, 5632 44 | 40). Rows of
 //   a multiple of 4096 bytes, of which 64 lines begin on the same channels, take 32
 //   whatever their length (4096: 99 | 108, 99 | 105, 111 | 113; 8192: 188 | 195, 94 | 103).
-// - up to 40 rows 32 and 64, for I only where there is one group (E, 64 tokens to 8 of 64
-//   experts of 2 x 2048 x 4096: 218, on tiles 234; I, more tokens a group: 277 and 269).
+// - up to 40 rows 32 and 64, for I only where there is one group (64 tokens to 8 of 64
+//   experts of 2 x 2048 x 4096: E 223, on tiles 231, I 202 and 215. Groups of unlike lengths
+//   lose, of which the rule knows nothing, and I the more: 640 rows in 16 random groups,
+//   2 x 8192 x 5120, E 428 and 273, I 387 and 238).
 // - tiles of 256 x 256, one a CU, or 128 x 128, two a CU: by the time of their
 //   rounds, in hundredths of a round of two tiles of 128 x 128 a CU. A tile of
 //   256 x 256 takes 1.47 of it and one of 128 x 128 alone on its CU 0.65 (I, 2048 x
